@@ -326,8 +326,7 @@ LS_API int ls_verify_attn_static(const void* q, const void* k_cache, const void*
  *   workspace    at least ls_tree_accept_workspace_size(dims, total_nodes) bytes, 256-byte
  *                aligned; holds per-segment maxima between the two kernels
  * Returns LS_OK, LS_ERR_INVALID_ARG, LS_ERR_UNSUPPORTED (tree_size > 128), LS_ERR_WORKSPACE
- * or LS_ERR_CUDA; asynchronous on `stream`. Sampling-based (non-greedy) verification is
- * not offered.
+ * or LS_ERR_CUDA; asynchronous on `stream`. ls_tree_accept_sample below is the sampled form.
  */
 enum { LS_DTYPE_BF16 = 0, LS_DTYPE_F32 = 1 };
 
@@ -343,6 +342,145 @@ LS_API int ls_tree_accept_greedy(const void* logits, const int32_t* tree_tokens,
                                  const int32_t* cu_tree, int32_t total_nodes, int32_t* accept_len,
                                  int32_t* accept_path, int32_t* next_token, const ls_accept_dims* dims,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A paged K/V cache held in 8 bits: codes of 8-bit floating point (e4m3: 4 exponent bits,
+ * 3 fraction bits, largest 448) with one fp32 scale for each block of tokens and kv head,
+ * keys and values apart (the LongSpec pages have no counterpart; it is the cache of
+ * ls_paged_kv at half its bytes, for contexts and batches whose cache bounds the step).
+ * Key j of sequence b lies in row r = page_table[b * max_pages_per_seq + j / page_size] *
+ * page_size + j % page_size, and stands for
+ *   k_pages[r, kh, :] * k_scale[r / scale_block, kh]      (values likewise)
+ *
+ *   page_size, max_pages_per_seq, num_pages, page_table   as in ls_paged_kv; an entry
+ *                  outside [0, num_pages) reads another page, or drops the rows of a write.
+ *                  max_pages_per_seq * page_size < 2^31.
+ *   scale_block    16, 32, 64 or 128, dividing page_size (else LS_ERR_UNSUPPORTED, or
+ *                  LS_ERR_INVALID_ARG where it does not divide)
+ *   k_pages, v_pages   [num_pages * page_size, H_kv, d] bytes, 16-byte aligned
+ *   k_scale, v_scale   fp32 [num_pages * page_size / scale_block, H_kv], finite and not
+ *                  negative; the attention counts a value scale outside [2^-60, 2^64] as
+ *                  the nearer end. Scales and rows past a sequence's end may hold anything.
+ */
+typedef struct {
+  int32_t page_size;
+  int32_t scale_block;
+  int32_t max_pages_per_seq;
+  int64_t num_pages;
+  const int32_t* page_table;
+  void* k_pages;
+  void* v_pages;
+  float* k_scale;
+  float* v_scale;
+} ls_kv_q8;
+
+/*
+ * ls_verify_attn_ex over an 8-bit paged cache: the same computation, options (per-sequence
+ * trees, window, RoPE; tree == NULL: none), results and errors, with the cached keys and
+ * values as ls_kv_q8 describes them. q, k_tree and v_tree are bf16 as there; tree_size = 1
+ * is a decoding step whose token is not in the cache yet. Tree values must be finite and
+ * below 2^78 in magnitude. Workspace: ls_verify_attn_q8_workspace_size(dims, tree) bytes.
+ * The weights enter the product with the values rounded to f16 (relative 2^-11); scores and
+ * sums are fp32. ls_verify_attn_check reads the device status.
+ */
+LS_API size_t ls_verify_attn_q8_workspace_size(const ls_verify_dims* dims, const ls_tree_opts* tree);
+LS_API int ls_verify_attn_q8(const void* q, const ls_kv_q8* kv, const void* k_tree, const void* v_tree,
+                             const int32_t* tree_parent, const int32_t* cu_seqlens, const ls_tree_opts* tree,
+                             void* out, float* lse, const ls_verify_dims* dims, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * ls_cross_attn over an 8-bit paged cache: every query attends its sequence's L_b cached
+ * keys and nothing else (a decoding step whose token was appended first, or the draft
+ * model's cross-attention); out = 0 and lse = -inf where L_b = 0.
+ */
+LS_API size_t ls_cross_attn_q8_workspace_size(const ls_verify_dims* dims);
+LS_API int ls_cross_attn_q8(const void* q, const ls_kv_q8* kv, const int32_t* cu_seqlens, void* out, float* lse,
+                            const ls_verify_dims* dims, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * New keys and values at the end of every sequence of an 8-bit cache, quantised.
+ *
+ * ls_kv_append_q8: rows cu_new[b] .. cu_new[b+1] - 1 of k_new / v_new (bf16
+ *   [total_new, H_kv, d]) become tokens L_b, L_b + 1, ... of sequence b, L_b =
+ *   cu_seqlens[b+1] - cu_seqlens[b] as before the call (prompts, chunks of them, or one
+ *   token each). max_new: the most rows that any sequence appends; rows past it are dropped.
+ * ls_kv_commit_q8: the accepted path of every verified tree, as the acceptance calls leave
+ *   it: tree rows accept_path[b, 0 .. accept_len[b]] (the root first; none where accept_len
+ *   is -1) of k_tree / v_tree, packed by cu_tree or dims->tree_size nodes each. A path entry
+ *   that is no node of its tree leaves its token as it was.
+ *
+ * For each scale block and head with new tokens: e = the least integer in [-60, 64] with
+ *   amax <= 448 * 2^e, amax the largest |x| of its new rows (NaN skipped). A block that
+ *   held tokens before keeps its scale where that is at least 2^e; else its codes are
+ *   rounded again, to c * (scale / 2^e), and its scale becomes 2^e. A block without earlier
+ *   tokens gets the scale 2^e whatever it held. code = x / scale rounded to nearest even,
+ *   saturated at +-448 (NaN stays NaN).
+ * The pages must be in the table already; no two sequences may share a page that is written.
+ * Tokens past max_pages_per_seq * page_size are dropped. No other row is touched.
+ *
+ *   cu_seqlens      device int32 [B+1]: lengths before the call
+ *   cu_seqlens_out  device int32 [B+1], not overlapping cu_seqlens, or NULL: written with
+ *                   the lengths after it (dropped tokens not counted)
+ *   dims            batch, num_kv_heads, head_dim (and tree_size for the commit) are used
+ * Returns LS_OK, LS_ERR_INVALID_ARG, LS_ERR_UNSUPPORTED or LS_ERR_CUDA; asynchronous on `stream`.
+ */
+LS_API int ls_kv_append_q8(const void* k_new, const void* v_new, const int32_t* cu_new, int32_t total_new,
+                           int32_t max_new, const int32_t* cu_seqlens, int32_t* cu_seqlens_out, const ls_kv_q8* kv,
+                           const ls_verify_dims* dims, void* stream);
+LS_API int ls_kv_commit_q8(const void* k_tree, const void* v_tree, const int32_t* cu_tree, int32_t total_nodes,
+                           const int32_t* accept_len, const int32_t* accept_path, const int32_t* cu_seqlens,
+                           int32_t* cu_seqlens_out, const ls_kv_q8* kv, const ls_verify_dims* dims, void* stream);
+
+/*
+ * Sampling: one token for each row of logits l, from a given uniform number u in [0, 1).
+ * With top = max l (NaN skipped) and t = temperature > 0, w_i = exp((l_i - top) / t); then,
+ * in the order of larger logit first and smaller index first among equals,
+ *   top_k keeps the first top_k entries (<= 0 or >= vocab: all);
+ *   top_p keeps, of those, every entry whose predecessors weigh less than top_p of their
+ *     sum, and always the first (>= 1: all);
+ *   min_p keeps the entries with w_i >= min_p (<= 0: all; above 1 counts as 1).
+ * token = the first kept i, in index order, with sum_{j <= i} w_j > u * (kept sum). Weights
+ * are held to 2^-43 of the largest and summed exactly, so the token is a function of the
+ * inputs alone. t <= 0 or NaN: greedy, the first index of the largest logit. A row without a
+ * logit above -inf gives 0; where the largest is +inf, only entries of +inf are drawn. u
+ * below 0 or NaN counts as 0, u >= 1 gives the last kept entry.
+ *
+ *   logits      [rows, vocab] bf16 or fp32 (LS_DTYPE_*), rows row_stride elements apart
+ *               (>= vocab); vocab up to 2^20. Rows that start on 16-byte boundaries are read
+ *               with 16-byte loads.
+ *   uniform     device fp32 [rows]
+ *   opts        arrays of one value per row (device; any may be NULL: temperature 1, the
+ *               others off), or NULL
+ *   out         device int32 [rows]
+ */
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} ls_sample_opts;
+
+LS_API int ls_sample(const void* logits, int64_t row_stride, const float* uniform, const ls_sample_opts* opts,
+                     int32_t* out, int64_t rows, int32_t vocab, int32_t logits_dtype, void* stream);
+
+/*
+ * Acceptance of a verified tree by sampling: the target's token at every node is drawn from
+ * its logits as ls_sample does (its own uniform number and options per node), and the walk
+ * moves from the root to the smallest child whose draft token is the current node's drawn
+ * token, until no child's is. Every token that the step yields was drawn from the target's
+ * own distribution given the accepted ones, so sampling stays lossless whatever the draft
+ * proposes; with temperature 0 it is ls_tree_accept_greedy. Arguments as there, except
+ *   uniform      device fp32 [N], opts: arrays of N values
+ *   node_token   device int32 [N], written: the token drawn at every node
+ *   accept_path  [B, T]: the entries after the path are written as -1
+ * and no workspace. The nodes' rows of logits are dense. LS_ERR_UNSUPPORTED: tree_size > 128
+ * or vocab > 2^20.
+ */
+LS_API int ls_tree_accept_sample(const void* logits, const float* uniform, const ls_sample_opts* opts,
+                                 const int32_t* tree_tokens, const int32_t* tree_parent, const int32_t* cu_tree,
+                                 int32_t total_nodes, int32_t* node_token, int32_t* accept_len, int32_t* accept_path,
+                                 int32_t* next_token, const ls_accept_dims* dims, void* stream);
 
 /*
  * Waits for `stream`, then reads the device-side status that the last ls_verify_attn

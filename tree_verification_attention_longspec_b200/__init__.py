@@ -17,4 +17,7 @@ def __getattr__(name):
     if name in ("verify_attn", "workspace_size", "VerifyAttn", "LSError", "load_library"):
         from . import binding
         return getattr(binding, name)
+    if name in ("KVCacheQ8", "VerifyAttnQ8", "CrossAttnQ8", "sample", "tree_accept_sample"):
+        from . import serving
+        return getattr(serving, name)
     raise AttributeError(name)

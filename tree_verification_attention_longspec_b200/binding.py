@@ -26,7 +26,9 @@ EXPORTED = ("ls_verify_attn", "ls_verify_attn_partials", "ls_verify_attn_combine
             "ls_verify_attn_workspace_size", "ls_verify_attn_check", "ls_status_string",
             "ls_verify_attn_plan", "ls_verify_attn_static", "ls_verify_attn_paged", "ls_cross_attn",
             "ls_cross_attn_workspace_size", "ls_verify_attn_ex", "ls_verify_attn_ex_workspace_size",
-            "ls_tree_accept_greedy", "ls_tree_accept_workspace_size")
+            "ls_tree_accept_greedy", "ls_tree_accept_workspace_size", "ls_verify_attn_q8",
+            "ls_verify_attn_q8_workspace_size", "ls_cross_attn_q8", "ls_cross_attn_q8_workspace_size",
+            "ls_kv_append_q8", "ls_kv_commit_q8", "ls_sample", "ls_tree_accept_sample")
 LS_DTYPE_BF16, LS_DTYPE_F32 = 0, 1
 
 
@@ -52,6 +54,20 @@ class TreeOpts(ctypes.Structure):
     and the limit of the kernel's device-side waits (0: the default, 4 s)."""
     _fields_ = [("cu_tree", ctypes.c_void_p), ("total_nodes", ctypes.c_int32), ("window", ctypes.c_int32),
                 ("rope_theta", ctypes.c_double), ("wait_limit_ns", ctypes.c_uint64)]
+
+
+class KvQ8(ctypes.Structure):
+    """ls_kv_q8: an 8-bit paged cache (device addresses of its table, codes and scales)."""
+    _fields_ = [("page_size", ctypes.c_int32), ("scale_block", ctypes.c_int32),
+                ("max_pages_per_seq", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class SampleOpts(ctypes.Structure):
+    """ls_sample_opts: device addresses of one value per row, or None."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p)]
 
 
 class AcceptDims(ctypes.Structure):
@@ -116,6 +132,23 @@ def _open(path: str):
     lib.ls_tree_accept_workspace_size.restype = ctypes.c_size_t
     lib.ls_tree_accept_greedy.argtypes = [P, P, P, P, ctypes.c_int32, P, P, P, A, P, ctypes.c_size_t, P]
     lib.ls_tree_accept_greedy.restype = ctypes.c_int
+    Q, O, I32, I64 = ctypes.POINTER(KvQ8), ctypes.POINTER(SampleOpts), ctypes.c_int32, ctypes.c_int64
+    lib.ls_verify_attn_q8_workspace_size.argtypes = [D, T]
+    lib.ls_verify_attn_q8_workspace_size.restype = ctypes.c_size_t
+    lib.ls_verify_attn_q8.argtypes = [P, Q, P, P, P, P, T, P, P, D, P, ctypes.c_size_t, P]
+    lib.ls_verify_attn_q8.restype = ctypes.c_int
+    lib.ls_cross_attn_q8_workspace_size.argtypes = [D]
+    lib.ls_cross_attn_q8_workspace_size.restype = ctypes.c_size_t
+    lib.ls_cross_attn_q8.argtypes = [P, Q, P, P, P, D, P, ctypes.c_size_t, P]
+    lib.ls_cross_attn_q8.restype = ctypes.c_int
+    lib.ls_kv_append_q8.argtypes = [P, P, P, I32, I32, P, P, Q, D, P]
+    lib.ls_kv_append_q8.restype = ctypes.c_int
+    lib.ls_kv_commit_q8.argtypes = [P, P, P, I32, P, P, P, P, Q, D, P]
+    lib.ls_kv_commit_q8.restype = ctypes.c_int
+    lib.ls_sample.argtypes = [P, I64, P, O, P, I64, I32, I32, P]
+    lib.ls_sample.restype = ctypes.c_int
+    lib.ls_tree_accept_sample.argtypes = [P, P, O, P, P, P, I32, P, P, P, P, A, P]
+    lib.ls_tree_accept_sample.restype = ctypes.c_int
     lib.ls_verify_attn_static.argtypes = [P, P, P, P, P, P, P, P, P, D, P]
     lib.ls_verify_attn_static.restype = ctypes.c_int
     lib.ls_verify_attn_workspace_size.argtypes = [D]

@@ -9,6 +9,7 @@
 
 #include "ls_device.cuh"
 #include "ls_verify_attn.h"
+#include "q8_device.cuh"
 
 namespace {
 
@@ -84,7 +85,9 @@ int check_tree(const ls_verify_dims* d, const ls_tree_opts* t) {
 // nearly equal length (none longer than C). The estimate is closed-form: the plan is
 // made on every call, so it must cost microseconds, not the milliseconds that simulating
 // the grid's schedule would.
-int make_plan(const ls_verify_dims* d, Plan* p, bool with_tree = true, const ls_tree_opts* tree = nullptr) {
+// slot_rows > 0: the plan of the 8-bit cache's kernel for few rows, whose units are that many rows.
+int make_plan(const ls_verify_dims* d, Plan* p, bool with_tree = true, const ls_tree_opts* tree = nullptr,
+              int32_t slot_rows = 0) {
   int rc = check_dims(d);
   if (rc != LS_OK) return rc;
   rc = check_tree(d, tree);
@@ -108,7 +111,8 @@ int make_plan(const ls_verify_dims* d, Plan* p, bool with_tree = true, const ls_
   q.wait_ns = (int64_t)(tree != nullptr && tree->wait_limit_ns > 0 ? tree->wait_limit_ns : kDefaultWaitNs);
   if (q.g > ls::kUnitRows) return LS_ERR_UNSUPPORTED;
   q.tpu = ls::kUnitRows / q.g;
-  q.rg = ls::ceil_div(q.T, q.tpu);
+  q.slot_rows = slot_rows;
+  q.rg = slot_rows > 0 ? ls::ceil_div(q.rows, slot_rows) : ls::ceil_div(q.T, q.tpu);
   q.scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)q.d);
   q.scale_log2 = (float)((double)q.scale * 1.4426950408889634074);
   // few output rows (a draft query or a small tree): one row per combine CTA, whose warps
@@ -412,6 +416,217 @@ int ls_verify_attn_ex(const void* q, const void* k_cache, const void* v_cache, c
                     workspace_bytes, stream, true, tree, &p);
   if (rc != LS_OK) return rc;
   return run_combine(cu_seqlens, out, lse, dims, workspace, workspace_bytes, stream, true, tree, &p);
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- the 8-bit cache
+
+// Rows of a unit: 8 where a kv head's rows fit them, else 16 (several units a head where
+// they do not fit those).
+int32_t q8_slot_rows(const ls_verify_dims* d) {
+  if (d == nullptr || d->num_kv_heads < 1) return 8;  // make_plan refuses it
+  const long long rows = (long long)d->tree_size * (d->num_q_heads / d->num_kv_heads);
+  return rows <= 8 ? 8 : 16;
+}
+
+int q8_plan(const ls_verify_dims* d, Plan* p, bool with_tree, const ls_tree_opts* tree) {
+  return make_plan(d, p, with_tree, tree, q8_slot_rows(d));
+}
+
+// Checks a cache description for `batch` sequences of at most max_len tokens.
+int check_kv(const ls_kv_q8* kv, int64_t max_len) {
+  if (kv == nullptr) return LS_ERR_INVALID_ARG;
+  const int32_t ps = kv->page_size, sb = kv->scale_block;
+  if (!(ps == 16 || ps == 32 || ps == 64 || (ps >= 128 && ps % 128 == 0 && ps <= (1 << 20)))) return LS_ERR_UNSUPPORTED;
+  if (!(sb == 16 || sb == 32 || sb == 64 || sb == 128)) return LS_ERR_UNSUPPORTED;
+  if (ps % sb != 0 || kv->max_pages_per_seq < 1 || kv->num_pages < 1) return LS_ERR_INVALID_ARG;
+  if (kv->num_pages > INT32_MAX || kv->num_pages * (int64_t)ps >= (int64_t)1 << 31) return LS_ERR_UNSUPPORTED;
+  if ((int64_t)kv->max_pages_per_seq * ps > INT32_MAX) return LS_ERR_UNSUPPORTED;  // positions stay int32
+  if (kv->page_table == nullptr || !aligned4(kv->page_table)) return LS_ERR_INVALID_ARG;
+  if (kv->k_pages == nullptr || kv->v_pages == nullptr || !aligned16(kv->k_pages) || !aligned16(kv->v_pages))
+    return LS_ERR_INVALID_ARG;
+  if (kv->k_scale == nullptr || kv->v_scale == nullptr || !aligned4(kv->k_scale) || !aligned4(kv->v_scale))
+    return LS_ERR_INVALID_ARG;
+  if ((max_len + ps - 1) / ps > kv->max_pages_per_seq) return LS_ERR_INVALID_ARG;
+  return LS_OK;
+}
+
+ls::KvQ8 kv_args(const ls_kv_q8* kv) {
+  ls::KvQ8 k;
+  k.k_pages = static_cast<uint8_t*>(kv->k_pages);
+  k.v_pages = static_cast<uint8_t*>(kv->v_pages);
+  k.k_scale = kv->k_scale;
+  k.v_scale = kv->v_scale;
+  k.page_table = kv->page_table;
+  k.page_size = kv->page_size;
+  k.scale_block = kv->scale_block;
+  k.max_pages = kv->max_pages_per_seq;
+  k.num_pages = (int32_t)kv->num_pages;
+  return k;
+}
+
+int run_q8(const void* q, const ls_kv_q8* kv, const void* k_tree, const void* v_tree, const int32_t* tree_parent,
+           const int32_t* cu_seqlens, const ls_tree_opts* tree, void* out, float* lse, const ls_verify_dims* dims,
+           void* workspace, size_t workspace_bytes, void* stream, bool with_tree) {
+  int rc = check_dims(dims);
+  if (rc == LS_OK) rc = check_tree(dims, tree);
+  if (rc != LS_OK) return rc;
+  int64_t max_len = dims->max_prefix_len;
+  if (dims->cu_seqlens_host)
+    for (int b = 0; b < dims->batch; ++b)
+      max_len = std::max<int64_t>(max_len, dims->cu_seqlens_host[b + 1] - dims->cu_seqlens_host[b]);
+  rc = check_kv(kv, max_len);
+  if (rc != LS_OK) return rc;
+  if (q == nullptr || !aligned16(q) || cu_seqlens == nullptr || !aligned4(cu_seqlens)) return LS_ERR_INVALID_ARG;
+  if (with_tree) {
+    if (k_tree == nullptr || v_tree == nullptr || !aligned16(k_tree) || !aligned16(v_tree)) return LS_ERR_INVALID_ARG;
+    if (tree_parent == nullptr || !aligned4(tree_parent)) return LS_ERR_INVALID_ARG;
+  }
+  if (out == nullptr || !aligned16(out) || lse == nullptr || !aligned4(lse)) return LS_ERR_INVALID_ARG;
+  Plan p;
+  rc = q8_plan(dims, &p, with_tree, tree);
+  if (rc != LS_OK) return rc;
+  const ls::Layout lay = ls::make_layout(p);
+  if (!workspace_ok(workspace, workspace_bytes, lay)) return LS_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  (void)cudaGetLastError();
+  ls::Q8Args a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_tree = static_cast<const uint16_t*>(k_tree);
+  a.v_tree = static_cast<const uint16_t*>(v_tree);
+  a.parent = tree_parent;
+  a.cu = cu_seqlens;
+  a.cu_tree = tree != nullptr ? tree->cu_tree : nullptr;
+  a.kv = kv_args(kv);
+  a.o_part = reinterpret_cast<float*>(ws + lay.o_part);
+  a.lse_part = reinterpret_cast<float*>(ws + lay.lse_part);
+  a.chunk_status = reinterpret_cast<uint32_t*>(ws + lay.chunk_status);
+  a.after_prep = 0;
+  a.p = p;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p.rope) {
+    ls::TreeRopeArgs ra;
+    ra.q = a.q;
+    ra.k_tree = a.k_tree;
+    ra.parent = tree_parent;
+    ra.cu = cu_seqlens;
+    ra.cu_tree = a.cu_tree;
+    ra.q_rot = reinterpret_cast<uint16_t*>(ws + lay.q_rot);
+    ra.k_rot = reinterpret_cast<uint16_t*>(ws + lay.k_rot);
+    ra.rope_status = reinterpret_cast<uint32_t*>(ws + lay.rope_status);
+    ra.log2_theta = std::log2(tree->rope_theta);
+    ra.p = p;
+    if (ls::launch_tree_rope(ra, st) != cudaSuccess) return LS_ERR_CUDA;
+    a.q = ra.q_rot;
+    a.k_tree = ra.k_rot;
+    a.after_prep = 1;
+  }
+  if (ls::launch_q8_rows(a, st) != cudaSuccess) return LS_ERR_CUDA;
+  return run_combine(cu_seqlens, out, lse, dims, workspace, workspace_bytes, stream, with_tree, tree, &p);
+}
+
+// What both writers of the cache share; arguments of the rows' source already checked.
+int run_append(ls::AppendArgs& a, const void* k_new, const void* v_new, const int32_t* cu_seqlens,
+               int32_t* cu_seqlens_out, const ls_kv_q8* kv, const ls_verify_dims* dims, int64_t rows, int32_t max_new,
+               void* stream) {
+  const int rk = check_kv(kv, 0);
+  if (rk != LS_OK) return rk;
+  if (cu_seqlens == nullptr || !aligned4(cu_seqlens) || !aligned4(cu_seqlens_out)) return LS_ERR_INVALID_ARG;
+  if (rows > 0 && max_new > 0 && (k_new == nullptr || v_new == nullptr)) return LS_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new)) return LS_ERR_INVALID_ARG;
+  // the lengths are read while the new ones are written
+  if (cu_seqlens_out != nullptr && cu_seqlens_out <= cu_seqlens + dims->batch &&
+      cu_seqlens <= cu_seqlens_out + dims->batch)
+    return LS_ERR_INVALID_ARG;
+  int sms = 0, major = 0;
+  const int rd = device_info(&sms, &major);
+  if (rd != LS_OK) return rd;
+  if (major != 10) return LS_ERR_UNSUPPORTED;
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.cu = cu_seqlens;
+  a.cu_out = cu_seqlens_out;
+  a.kv = kv_args(kv);
+  a.B = dims->batch;
+  a.Hkv = dims->num_kv_heads;
+  a.d = dims->head_dim;
+  a.rows = (int32_t)rows;
+  // a sequence cannot append more than its table has room for
+  a.max_new = (int32_t)std::min<int64_t>(max_new, (int64_t)kv->max_pages_per_seq * kv->page_size);
+  a.blocks = a.max_new > 0 ? (a.max_new - 1) / kv->scale_block + 2 : 0;
+  (void)cudaGetLastError();
+  return ls::launch_q8_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LS_OK : LS_ERR_CUDA;
+}
+
+int check_append_dims(const ls_verify_dims* d) {
+  if (d == nullptr || d->batch < 1 || d->num_kv_heads < 1) return LS_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return LS_ERR_UNSUPPORTED;
+  return LS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ls_verify_attn_q8_workspace_size(const ls_verify_dims* dims, const ls_tree_opts* tree) {
+  Plan p;
+  if (q8_plan(dims, &p, true, tree) != LS_OK) return 0;
+  return (size_t)ls::make_layout(p).total;
+}
+
+int ls_verify_attn_q8(const void* q, const ls_kv_q8* kv, const void* k_tree, const void* v_tree,
+                      const int32_t* tree_parent, const int32_t* cu_seqlens, const ls_tree_opts* tree, void* out,
+                      float* lse, const ls_verify_dims* dims, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_q8(q, kv, k_tree, v_tree, tree_parent, cu_seqlens, tree, out, lse, dims, workspace, workspace_bytes,
+                stream, true);
+}
+
+size_t ls_cross_attn_q8_workspace_size(const ls_verify_dims* dims) {
+  Plan p;
+  if (q8_plan(dims, &p, false, nullptr) != LS_OK) return 0;
+  return (size_t)ls::make_layout(p).total;
+}
+
+int ls_cross_attn_q8(const void* q, const ls_kv_q8* kv, const int32_t* cu_seqlens, void* out, float* lse,
+                     const ls_verify_dims* dims, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_q8(q, kv, nullptr, nullptr, nullptr, cu_seqlens, nullptr, out, lse, dims, workspace, workspace_bytes,
+                stream, false);
+}
+
+int ls_kv_append_q8(const void* k_new, const void* v_new, const int32_t* cu_new, int32_t total_new, int32_t max_new,
+                    const int32_t* cu_seqlens, int32_t* cu_seqlens_out, const ls_kv_q8* kv, const ls_verify_dims* dims,
+                    void* stream) {
+  const int rc = check_append_dims(dims);
+  if (rc != LS_OK) return rc;
+  if (total_new < 0 || max_new < 0 || cu_new == nullptr || !aligned4(cu_new)) return LS_ERR_INVALID_ARG;
+  ls::AppendArgs a{};
+  a.cu_new = cu_new;
+  return run_append(a, k_new, v_new, cu_seqlens, cu_seqlens_out, kv, dims, total_new, std::min(max_new, total_new),
+                    stream);
+}
+
+int ls_kv_commit_q8(const void* k_tree, const void* v_tree, const int32_t* cu_tree, int32_t total_nodes,
+                    const int32_t* accept_len, const int32_t* accept_path, const int32_t* cu_seqlens,
+                    int32_t* cu_seqlens_out, const ls_kv_q8* kv, const ls_verify_dims* dims, void* stream) {
+  const int rc = check_append_dims(dims);
+  if (rc != LS_OK) return rc;
+  if (dims->tree_size < 1) return LS_ERR_INVALID_ARG;
+  if (dims->tree_size > ls::kMaxTree) return LS_ERR_UNSUPPORTED;
+  const int64_t most = (int64_t)dims->batch * dims->tree_size;
+  if (most > (1ll << 30)) return LS_ERR_UNSUPPORTED;
+  const int64_t nodes = cu_tree != nullptr ? (int64_t)total_nodes : most;
+  if (nodes < 0 || nodes > most || !aligned4(cu_tree)) return LS_ERR_INVALID_ARG;
+  if (accept_len == nullptr || accept_path == nullptr || !aligned4(accept_len) || !aligned4(accept_path))
+    return LS_ERR_INVALID_ARG;
+  ls::AppendArgs a{};
+  a.accept_len = accept_len;
+  a.accept_path = accept_path;
+  a.cu_tree = cu_tree;
+  a.T = dims->tree_size;
+  return run_append(a, k_tree, v_tree, cu_seqlens, cu_seqlens_out, kv, dims, nodes, dims->tree_size, stream);
 }
 
 int ls_verify_attn_check(const ls_verify_dims* dims, const void* workspace, void* stream) {

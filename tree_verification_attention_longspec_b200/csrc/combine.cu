@@ -81,10 +81,10 @@ __global__ void __maxnreg__(112) combine_kernel(const __grid_constant__ CombineA
     int32_t u, r;
     unit_row(p, i, j, &u, &r);
     rl = r;
-    alt = unit_alternates(min(p.tpu, tree_n - u * p.tpu) * p.g);
+    alt = p.slot_rows == 0 && unit_alternates(min(p.tpu, tree_n - u * p.tpu) * p.g);
     cbase = first + (kh * p.rg + u) * n;
     // the row's chunks, its output row and (with RoPE) the tree kernel's word of its node
-    LS_DCHECK(err, b < p.B && kh < p.Hkv && u < p.rg && r < kUnitRows);
+    LS_DCHECK(err, b < p.B && kh < p.Hkv && u < p.rg && r < unit_slot(p));
     LS_DCHECK(err, !(writes && lengths_ok) || (cbase >= 0 && cbase + n <= p.n_chunks));
     LS_DCHECK(err, !writes || (tree_base + i < p.N && out_row < (int64_t)p.N * p.Hq));
 #if defined(LS_DEBUG)
@@ -104,9 +104,10 @@ __global__ void __maxnreg__(112) combine_kernel(const __grid_constant__ CombineA
       // slot) when the partials kernel's tiles alternated key blocks
       const int sh = alt ? 1 : 0;
       const int n_parts = n << sh;
-      const size_t row0 = (size_t)cbase * kUnitRows + rl;
+      const int slot = unit_slot(p);
+      const size_t row0 = (size_t)cbase * slot + rl;
       auto part_row = [&](int k) -> size_t {  // row of partial k in o_part / lse_part
-        return row0 + (uint32_t)((k >> sh) * kUnitRows + ((k & sh) << 7));
+        return row0 + (uint32_t)((k >> sh) * slot + ((k & sh) << 7));
       };
       // a wide CTA's warp w takes the batches w, w + 4, ...
       const int first_batch = wide ? warp * kPrefetch : 0, stride = wide ? kMergeRows * kPrefetch : kPrefetch;
@@ -116,7 +117,7 @@ __global__ void __maxnreg__(112) combine_kernel(const __grid_constant__ CombineA
         float lx = -INFINITY;
         if (lane < nx) {
           LS_DCHECK(err, cbase + ((x0 + lane) >> sh) < p.n_chunks &&
-                             part_row(x0 + lane) < (size_t)p.n_chunks * kUnitRows);
+                             part_row(x0 + lane) < (size_t)p.n_chunks * slot);
           lx = a.lse_part[part_row(x0 + lane)];
           err |= a.chunk_status[cbase + ((x0 + lane) >> sh)];
         }

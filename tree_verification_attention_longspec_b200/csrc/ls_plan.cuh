@@ -59,7 +59,9 @@ struct Plan {
   int32_t window;      // > 0: sliding window of this many positions; 0: the whole prefix
   int32_t rows;        // T * g query rows per (sequence, kv head)
   int32_t tpu;         // tree nodes per unit: floor(kUnitRows / g)
-  int32_t rg;          // units per (sequence, kv head): ceil(T / tpu)
+  int32_t rg;          // units per (sequence, kv head): ceil(T / tpu), or ceil(rows / slot_rows)
+  int32_t slot_rows;   // > 0: units of this many rows, node boundaries aside (the 8-bit cache's
+                       // kernel for few rows); 0: kUnitRows, whole nodes
   int32_t C;           // 128-key blocks per chunk
   int32_t with_tree;   // 1: every key list ends with the tree block; 0: prefix keys only
   int32_t uniform_n;   // >= 0: chunks per unit for every sequence; -1: from L_b
@@ -142,8 +144,16 @@ LS_HD bool tree_range(const Plan& p, const int32_t* cu_tree, int32_t b, int32_t*
 // chunk's slot).
 LS_HD bool unit_alternates(int32_t rows_here) { return rows_here <= 128; }
 
+// Rows of a unit's slot in o_part / lse_part.
+LS_HD int32_t unit_slot(const Plan& p) { return p.slot_rows > 0 ? p.slot_rows : kUnitRows; }
+
 // Unit and row inside the unit of query row (tree node i, head-in-group j).
 LS_HD void unit_row(const Plan& p, int32_t i, int32_t j, int32_t* unit, int32_t* row) {
+  if (p.slot_rows > 0) {
+    *unit = (i * p.g + j) / p.slot_rows;
+    *row = i * p.g + j - *unit * p.slot_rows;
+    return;
+  }
   *unit = i / p.tpu;
   *row = (i - *unit * p.tpu) * p.g + j;
 }
@@ -214,8 +224,8 @@ LS_HD void sequence_chunks(const Plan& p, const int32_t* cu, int32_t b, int32_t*
 // first, so that their place depends on the output rows alone, not on the chunk plan.
 struct Layout {
   uint64_t status;        // u32   [n_combine]
-  uint64_t o_part;        // float [n_chunks][kUnitRows][d]   partial out, normalised
-  uint64_t lse_part;      // float [n_chunks][kUnitRows]      partial lse, log2 domain
+  uint64_t o_part;        // float [n_chunks][unit_slot][d]   partial out, normalised
+  uint64_t lse_part;      // float [n_chunks][unit_slot]      partial lse, log2 domain
   uint64_t chunk_status;  // u32   [n_chunks]
   uint64_t q_rot;         // bf16  [N][Hq][d]    rotated queries (rope only)
   uint64_t k_rot;         // bf16  [N][Hkv][d]   rotated tree keys (rope only)
@@ -231,9 +241,9 @@ LS_HD Layout make_layout(const Plan& p) {
   l.status = off;
   off = align256(off + (uint64_t)p.n_combine * 4);
   l.o_part = off;
-  off = align256(off + (uint64_t)p.n_chunks * kUnitRows * p.d * 4);
+  off = align256(off + (uint64_t)p.n_chunks * unit_slot(p) * p.d * 4);
   l.lse_part = off;
-  off = align256(off + (uint64_t)p.n_chunks * kUnitRows * 4);
+  off = align256(off + (uint64_t)p.n_chunks * unit_slot(p) * 4);
   l.chunk_status = off;
   off = align256(off + (uint64_t)p.n_chunks * 4);
   const uint64_t nq = p.rope ? (uint64_t)p.N * p.Hq * p.d * 2 : 0, nk = p.rope ? (uint64_t)p.N * p.Hkv * p.d * 2 : 0;
