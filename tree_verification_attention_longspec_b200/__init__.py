@@ -19,5 +19,6 @@ def __getattr__(name):
         return getattr(binding, name)
     if name in ("KVCacheQ8", "VerifyAttnQ8", "CrossAttnQ8", "sample", "tree_accept_sample"):
         from . import serving
-        return getattr(serving, name)
+        globals()[name] = value = getattr(serving, name)  # found without this call from now on
+        return value
     raise AttributeError(name)

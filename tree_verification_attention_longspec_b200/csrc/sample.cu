@@ -12,15 +12,26 @@
 //
 // Weights are integers, round(w * 2^43): sums of them are exact in 64 bits (2^20 entries
 // at most), so they come out the same in any order, atomics included, and the token is a
-// function of the inputs alone. w itself is computed in fp64 (relative error below 2^-46):
+// function of the inputs alone. w itself is computed in fp64 (relative error below 2^-41):
 // an fp32 exponential's 1e-7 would move the borders of a flat 128k-entry distribution by
 // more than the gap that one row in a thousand leaves to its uniform number.
 //
 // One cluster of 1 to 8 CTAs per row; each keeps its share of the row in shared memory
 // (what does not fit is read again), so that HBM is read once, and the passes over it
-// meet through distributed shared memory. A threshold is found by a histogram of 1024
-// bins, linear in the distance to the largest logit, then by further ones over the keys
-// of the one bin that holds the border, whose members are listed aside.
+// meet through distributed shared memory:
+//   load       the largest logit;
+//   histogram  (top-k or top-p) entries counted in 4096 bins of x = (top - l) / t. Counts
+//              give top-k's border bin; with each bin's largest and smallest weight they
+//              bound where top-p's border lies, with its middle one they guess it;
+//   weigh      the exact sums above and below those bins, whose own entries are listed;
+//   resolve    every CTA sorts the cluster's list (bitonic, 64-bit (key, index)), finds the
+//              last entry kept, then the CTA, the warp's run and the entry that the uniform
+//              number falls on. Only the CTA that owns it weighs that run again. The exact
+//              sums show whether the listed bins did hold the border.
+// The weights' fp64 arithmetic bounds it (10 instructions an entry where the whole sum is
+// needed); the histogram takes one shared-memory atomic an entry. Rows whose border bins
+// hold more entries than the list (long runs of equal logits), or missed the border, take
+// `select` instead: exact histograms of the weights, level by level down to one key.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -48,21 +59,27 @@ struct SampleArgs {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;  // two CTAs an SM: one's loads run under the other's arithmetic
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = kThreads;  // one per thread
-constexpr int kList = 4096;      // keys of a border bin kept aside
+constexpr int kBins = kThreads;  // of `select`: one per thread
+constexpr int kFine = 4096;      // bins of the first histogram
+constexpr int kFinePer = kFine / kThreads;
+constexpr int kFineUnit = 128;   // of them for one unit of x, where x spans the weights' whole range
+constexpr int kList = 1024;      // entries of the border bins kept aside, two per thread
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 20;  // sums of 2^43 stay below 2^63
 constexpr int kWeightBits = 43;
+constexpr float kMaxX = 30.6f;  // exp(-30.6) is below half a unit
 // a weight's three parts: a CTA's share is at most 2^17 entries, so their sums fit 32 bits
 constexpr int kPartBits = 15;
 constexpr int kMaxSeg = 1 << 17;
-constexpr int kDataBytes = 160 * 1024;
+constexpr int kLut = 1024;  // e^(-b / 32) * 2^43
+constexpr int kDataBytes = 76 * 1024;
 
 using u64 = unsigned long long;
 
-// Order-preserving key of a float: larger value, larger key (-0 and +0 get one key).
+// Order-preserving key of a float: larger value, larger key (-0 and +0 get one key). NaN has
+// no place in it: its weight is 0, and where entries are counted it is taken for -inf.
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
@@ -70,53 +87,65 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+__device__ __forceinline__ uint32_t order_key(float x) { return key_of(x == x ? x : -INFINITY); }
 
-struct Shared {
+// Place of an entry in the order: larger key first, then smaller index.
+__device__ __forceinline__ u64 place_of(uint32_t key, uint32_t i) { return ((u64)~key << 32) | i; }
+
+// The two ways to a row's threshold share the memory (a cluster barrier lies between).
+struct Fast {
+  uint32_t hist[kFine];  // later the sorted list (u64[kList])
+  u64 list[kList];
+};
+struct Slow {
   u64 hist[kBins];          // this CTA's measure of each bin
   uint32_t part[3][kBins];  // its parts while they are added up
   uint32_t list[kList];
-  uint32_t n_list;
-  uint32_t kmin, kmax;  // keys of the border bin
-  u64 wsum[kWarps + 1];
-  u64 total;  // this CTA's sum
-  u64 above;  // measure before the border bin, and in it
-  u64 inside;
-  uint32_t bin;
-  float fmax[kWarps], fmin[kWarps];
-  float top, low;
-  uint32_t cut;  // index threshold found by the CTA that owns it
+};
+static_assert(sizeof(uint32_t) * kFine >= sizeof(u64) * kList && kList == 2 * kThreads, "sorted list");
+
+// What the first histogram tells: top-k's border bin (kFine - 1: none) with the entries
+// before it and in it, and the bins [lo, hi] that should hold top-p's border.
+struct Borders {
+  int bk;
+  uint32_t above, in;
+  int lo, hi;
+};
+// What the list decides: the place of the last entry kept, and the CTA whose share holds the
+// target, with the sum before it. ok = 0: nothing (the list is too short, or elsewhere).
+struct Verdict {
+  u64 last, target, pre;
+  int ok, owner;
 };
 
-// 2^43 * exp(x) rounded, x <= 0. exp by 2^n * 2^f, f in [-1/2, 1/2], and the Taylor
-// polynomial of 2^f = exp(f ln 2) to degree 11 (remainder (ln2/2)^12/12! = 6e-15).
-__device__ __forceinline__ u64 weight_of(double x) {
-  if (!(x > -30.6)) return 0ull;  // below half a unit
-  const double magic = 6755399441055744.0;  // 1.5 * 2^52
-  const double y = x * 1.4426950408889634074;
-  const double t = y + magic;
-  const int n = __double2loint(t);
-  const double f = y - (t - magic);
-  double p = 4.4455382718708100e-10;  // (ln 2)^k / k!, k = 11 .. 0
-  p = fma(p, f, 7.0549116208011210e-09);
-  p = fma(p, f, 1.0178086009239696e-07);
-  p = fma(p, f, 1.3215486790144305e-06);
-  p = fma(p, f, 1.5252733804059838e-05);
-  p = fma(p, f, 1.5403530393381606e-04);
-  p = fma(p, f, 1.3333558146428441e-03);
-  p = fma(p, f, 9.6181291076284770e-03);
-  p = fma(p, f, 5.5504108664821576e-02);
-  p = fma(p, f, 2.4022650695910070e-01);
-  p = fma(p, f, 6.9314718055994530e-01);
-  p = fma(p, f, 1.0);
-  return __double2ull_rn(p * __hiloint2double((1023 + kWeightBits + n) << 20, 0));
-}
+struct Shared {
+  double lut[kLut];
+  union {
+    Fast f;
+    Slow s;
+  };
+  u64 wsum[kWarps], scan[kWarps];
+  u64 total;          // this CTA's sum
+  u64 ws[3][kWarps];  // the warps' sums of `resolve`: kept for certain, under min-p, below the border
+  u64 tot[3];         // and the CTA's
+  u64 above, inside;  // measure before the border bin, and in it
+  u64 last, before;
+  Borders borders;
+  Verdict verdict;
+  uint32_t lpart[3][kWarps], cpart[3][kWarps];  // kept weights of the list, by run of this CTA and by CTA
+  uint32_t n_list, kmin, kmax;                  // listed entries; `select`: keys of the border bin
+  uint32_t bin, bins[3], in_range[2], cut;
+  uint32_t cwarp[kWarps];
+  float fmax[kWarps], fmin[kWarps], fsum[kWarps];
+  float top, low;
+};
 
 template <bool F32>
 struct Row {
   const void* g;      // this CTA's share in global memory
   const void* s;      // its first `cap` entries in shared memory
   int n, cap;
-  // entries i and i + 1 (i even); -inf past the share and for NaN
+  // entries i and i + 1 (i even); -inf past the share
   __device__ __forceinline__ void pair(int i, float& a, float& b) const {
     if (i + 1 < cap) {
       if constexpr (F32) {
@@ -133,13 +162,36 @@ struct Row {
     a = i < n ? load(i) : -INFINITY;
     b = i + 1 < n ? load(i + 1) : -INFINITY;
   }
-  __device__ __forceinline__ float load(int i) const {
-    float x;
+  // entries i .. of 16 bytes, all in shared memory
+  __device__ __forceinline__ void vector(int i, float (&x)[F32 ? 4 : 8]) const {
+    if constexpr (F32) {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(s) + i);
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s) + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ float one(int i) const {
+    if (i >= cap) return load(i);
     if constexpr (F32)
-      x = static_cast<const float*>(g)[i];
+      return static_cast<const float*>(s)[i];
     else
-      x = bf16_to_f32(static_cast<const uint16_t*>(g)[i]);
-    return x == x ? x : -INFINITY;
+      return bf16_to_f32(static_cast<const uint16_t*>(s)[i]);
+  }
+  __device__ __forceinline__ float load(int i) const {
+    if constexpr (F32)
+      return static_cast<const float*>(g)[i];
+    else
+      return bf16_to_f32(static_cast<const uint16_t*>(g)[i]);
   }
 };
 
@@ -148,6 +200,33 @@ struct Keep {
   uint32_t key, index;
   __device__ __forceinline__ bool has(uint32_t k, uint32_t i) const { return k > key || (k == key && i <= index); }
 };
+
+// sum += w where a < b (and c >= d): one predicated addition, w having been computed anyway.
+__device__ __forceinline__ void add_below(double& sum, double w, float a, float b) {
+  asm("{\n\t.reg .pred p;\n\tsetp.lt.f32 p, %2, %3;\n\t@p add.rn.f64 %0, %0, %1;\n\t}"
+      : "+d"(sum)
+      : "d"(w), "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add_below(double& sum, double w, float a, float b, float c, float d) {
+  asm("{\n\t.reg .pred p;\n\tsetp.lt.f32 p, %2, %3;\n\tsetp.ge.and.f32 p, %4, %5, p;\n\t@p add.rn.f64 %0, %0, %1;\n\t}"
+      : "+d"(sum)
+      : "d"(w), "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
+__device__ __forceinline__ u64 warp_sum64(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <class T>
+__device__ __forceinline__ T warp_scan(T v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
+  }
+  return v;
+}
 
 template <bool F32>
 class Sampler {
@@ -164,15 +243,17 @@ class Sampler {
     r_.g = F32 ? static_cast<const void*>(static_cast<const float*>(a.logits) + at)
                : static_cast<const void*>(static_cast<const uint16_t*>(a.logits) + at);
     r_.s = data;
-    // each warp's run of entries, in index order; two entries a lane and step
-    const int per = (r_.n + kWarps - 1) / kWarps;
-    run_ = (per + 63) / 64 * 64;
+    // each warp's run of entries, in index order: whole steps of 16-byte reads where it is long
+    const int per = (r_.n + kWarps - 1) / kWarps, whole = per >= 16 * 64 ? 32 * kPer : 64;
+    run_ = (per + whole - 1) / whole * whole;
     w0_ = min(r_.n, warp_ * run_);
     w1_ = min(r_.n, w0_ + run_);
   }
 
   __device__ void run() {
     load();
+    for (int i = tid_; i < kLut; i += kThreads) sh_.lut[i] = exp(-(double)i / 32.0) * (double)(1ull << kWeightBits);
+    extremes();
     const float t = a_.temperature != nullptr ? a_.temperature[row_id_] : 1.0f;
     if (top_ == -INFINITY) {  // nothing above -inf
       if (rank_ == 0 && tid_ == 0) a_.out[row_id_] = 0;
@@ -183,116 +264,142 @@ class Sampler {
       auto first = [top](float x, uint32_t) { return x == top ? 1ull : 0ull; };
       u64 before;
       sums(first, &before);
-      const int i = find(first, before, 0ull);
+      const int i = find(first, before, 0ull, w0_, w1_, sh_.wsum[warp_]);
       if (i >= 0) a_.out[row_id_] = i;
       return;
     }
     inv_t_ = 1.0 / (double)t;
-    Keep keep{0u, 0xffffffffu};
-    const int k = a_.top_k != nullptr ? a_.top_k[row_id_] : 0;
-    if (k > 0 && k < a_.V) keep = select<false>(keep, top_ - low_, (u64)k, 0.0);
+    inv_f_ = (float)inv_t_;
+    top_d_ = (double)top_;
+    int k = a_.top_k != nullptr ? a_.top_k[row_id_] : 0;
+    if (k <= 0 || k >= a_.V) k = 0;
     const float p = a_.top_p != nullptr ? a_.top_p[row_id_] : 1.0f;
+    const uint32_t least = least_key(a_.min_p != nullptr ? a_.min_p[row_id_] : 0.0f, t);
+    const float u = a_.uniform[row_id_];
+    if (resolve(k, p, least, u)) return;
+    cl_.sync();  // the memory changes hands
+    Keep keep{0u, 0xffffffffu};
+    if (k > 0) keep = select<false>(keep, top_ - low_, (u64)k, 0.0);
     if (p < 1.0f) keep = select<true>(keep, fminf(31.0f * t, top_ - low_), 0ull, (double)p);
-    const float mp = a_.min_p != nullptr ? a_.min_p[row_id_] : 0.0f;
-    const double x_min = mp > 0.f ? (mp < 1.f ? log((double)mp) : 0.0) : -1e300;
-    auto kept = [this, keep, x_min](float x, uint32_t i) {
-      if (!keep.has(key_of(x), i)) return 0ull;
-      const double e = exponent(x);
-      return e >= x_min ? weight_of(e) : 0ull;
+    auto kept = [this, keep, least](float x, uint32_t i) {
+      const uint32_t key = key_of(x);
+      return key >= least && keep.has(key, i) ? weight_any(x) : 0ull;
     };
     u64 before;
     const u64 z = sums(kept, &before);
-    const float u = a_.uniform[row_id_];
-    const double at = u > 0.f ? (double)u * (double)z : 0.0;
-    const u64 target = at < (double)z ? min((u64)at, z - 1) : z - 1;
-    const int i = find(kept, before, target);
+    const int i = find(kept, before, target_of(u, z), w0_, w1_, sh_.wsum[warp_]);
     if (i >= 0) a_.out[row_id_] = i;
   }
 
  private:
+  static constexpr int kPer = F32 ? 4 : 8;  // entries of 16 bytes
   const SampleArgs& a_;
   Shared& sh_;
   cg::cluster_group cl_;
   int tid_, lane_, warp_, rank_, size_, lo_, run_, w0_, w1_;
   int64_t row_id_;
   Row<F32> r_;
-  float top_, low_;  // largest value; smallest above -inf
-  double inv_t_;
+  float top_, low_;  // largest and smallest logit
 
-  // (l - top) / t; 0 for the largest (also +inf), -inf for -inf
-  __device__ __forceinline__ double exponent(float x) const {
-    if (x == top_) return 0.0;
-    if (x == -INFINITY || top_ == INFINITY) return -INFINITY;
-    return ((double)x - (double)top_) * inv_t_;
+  double inv_t_, top_d_;
+  float inv_f_;
+
+  // round(2^43 exp((l - top) / t)), as a double, where x = (top - l) / t is below 32 (xf: x in
+  // fp32). exp(-x) = e^(-b / 32) * e^r with b the integer nearest to 32 x, |r| <= 2^-6, the
+  // first factor from a table and the second by its Taylor polynomial to degree 5
+  // (remainder 2^-36 / 720 = 2^-45). Adding and taking off 2^52 rounds to an integer.
+  __device__ __forceinline__ double weight_in(float l, float xf) const {
+    const int b = __float_as_int(fmaf(fminf(xf, 31.9f), 32.0f, 12582912.0f)) - 0x4b400000;
+    const double fb = __hiloint2double(0x42e00000, b) - 140737488355328.0;  // (2^47 + b / 32) - 2^47
+    const double r = fma((double)l - top_d_, inv_t_, fb);
+    double e = fma(r, 1.0 / 120.0, 1.0 / 24.0);
+    e = fma(e, r, 1.0 / 6.0);
+    e = fma(e, r, 0.5);
+    e = fma(e, r, 1.0);
+    e = fma(e, r, 1.0);
+    return fma(e, sh_.lut[b], 4503599627370496.0) - 4503599627370496.0;
+  }
+  // 0 beyond the range, and for NaN: of l, or of -inf under an infinite temperature
+  __device__ __forceinline__ u64 weight(float l) const {
+    const float xf = (top_ - l) * inv_f_;
+    return xf < kMaxX ? (u64)weight_in(l, xf) : 0ull;
+  }
+  // The same for the rows that `resolve` leaves to `select`: top_ may be +inf.
+  __device__ __forceinline__ u64 weight_any(float l) const { return l == top_ ? 1ull << kWeightBits : weight(l); }
+
+  __device__ __forceinline__ static u64 target_of(float u, u64 z) {
+    const double at = u > 0.f ? (double)u * (double)z : 0.0;
+    return at < (double)z ? min((u64)at, z - 1) : z - 1;
   }
 
-  // f(value, entry of the row) over this warp's run, two entries a lane and step
+  // The least key that min-p keeps: exp((l - top) / t) >= m, in fp64, for no lesser one.
+  __device__ uint32_t least_key(float m, float t) const {
+    if (!(m > 0.f) || top_ == INFINITY) return 0u;
+    const double x_min = m < 1.f ? log((double)m) : 0.0;
+    auto keeps = [&](uint32_t key) { return ((double)of_key(key) - top_d_) * inv_t_ >= x_min; };
+    uint32_t key = key_of((float)(top_d_ + x_min * (double)t));  // off by rounding
+    const uint32_t most = key_of(top_);
+    for (int i = 0; i < 4 && key < most && !keeps(key); ++i) ++key;
+    for (int i = 0; i < 4 && keeps(key - 1); ++i) --key;
+    return min(key, most);
+  }
+
+  // f(values, entry of the first) over this warp's run, 16 bytes a lane and step (NaN, which
+  // weighs nothing, beyond its end)
+  template <class F>
+  __device__ __forceinline__ void each_vector(F f) const {
+    const int whole = w0_ + max(0, min(w1_, r_.cap) - w0_) / kPer * kPer;
+    float x[kPer];
+    for (int i = w0_ + kPer * lane_; i < whole; i += 32 * kPer) {
+      r_.vector(i, x);
+      f(x, (uint32_t)(lo_ + i));
+    }
+#pragma unroll
+    for (int e = 1; e < kPer; ++e) x[e] = __uint_as_float(0x7fffffffu);
+    for (int i = whole + lane_; i < w1_; i += 32) {
+      x[0] = r_.one(i);
+      f(x, (uint32_t)(lo_ + i));
+    }
+  }
+  // f(value, entry of the row) over this warp's run
   template <class F>
   __device__ __forceinline__ void each(F f) const {
-    for (int i = w0_ + 2 * lane_; i < w1_; i += 64) {
-      float x, y;
-      r_.pair(i, x, y);
-      f(x, (uint32_t)(lo_ + i));
-      if (i + 1 < w1_) f(y, (uint32_t)(lo_ + i + 1));
+    const int whole = w0_ + max(0, min(w1_, r_.cap) - w0_) / kPer * kPer;
+    for (int i = w0_ + kPer * lane_; i < whole; i += 32 * kPer) {
+      float x[kPer];
+      r_.vector(i, x);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) f(x[e], (uint32_t)(lo_ + i + e));
+    }
+    for (int i = whole + lane_; i < w1_; i += 32) f(r_.one(i), (uint32_t)(lo_ + i));
+  }
+
+  // Starts the copy of the share into shared memory; `extremes` waits for it.
+  __device__ void load() {
+    const int n_vec = a_.vec ? r_.cap / kPer : 0;
+    uint8_t* to = static_cast<uint8_t*>(const_cast<void*>(r_.s));
+    const uint8_t* from = static_cast<const uint8_t*>(r_.g);
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    for (int v = tid_; v < n_vec; v += kThreads)
+      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(at + 16 * v), "l"(from + 16 * (int64_t)v) : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (int i = n_vec * kPer + tid_; i < r_.cap; i += kThreads) {
+      if constexpr (F32)
+        reinterpret_cast<float*>(to)[i] = static_cast<const float*>(r_.g)[i];
+      else
+        reinterpret_cast<uint16_t*>(to)[i] = static_cast<const uint16_t*>(r_.g)[i];
     }
   }
 
-  // The share into shared memory, and the row's largest and smallest finite-or-+inf value.
-  __device__ void load() {
+  // The row's largest and smallest logit (NaN skipped).
+  __device__ void extremes() {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
     float mx = -INFINITY, mn = INFINITY;
-    auto take = [&](float x) {
+    each([&](float x, uint32_t) {
       mx = fmaxf(mx, x);
-      if (x > -INFINITY) mn = fminf(mn, x);
-    };
-    constexpr int kPer = F32 ? 4 : 8;
-    const int n_vec = a_.vec ? r_.cap / kPer : 0;
-    constexpr int kFly = 4;
-    for (int v0 = tid_; v0 < n_vec; v0 += kFly * kThreads) {
-      uint4 w[kFly];
-#pragma unroll
-      for (int u = 0; u < kFly; ++u)
-        if (v0 + u * kThreads < n_vec) w[u] = __ldcs(static_cast<const uint4*>(r_.g) + v0 + u * kThreads);
-#pragma unroll
-      for (int u = 0; u < kFly; ++u) {
-        if (v0 + u * kThreads < n_vec) {
-          uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (F32) {
-              float x = __uint_as_float(q[e]);
-              if (!(x == x)) {
-                x = -INFINITY;
-                q[e] = 0xff800000u;
-              }
-              take(x);
-            } else {
-              float x = __uint_as_float(q[e] << 16), y = __uint_as_float(q[e] & 0xffff0000u);
-              if (!(x == x)) {
-                x = -INFINITY;
-                q[e] = (q[e] & 0xffff0000u) | 0xff80u;
-              }
-              if (!(y == y)) {
-                y = -INFINITY;
-                q[e] = (q[e] & 0xffffu) | 0xff800000u;
-              }
-              take(x);
-              take(y);
-            }
-          }
-          reinterpret_cast<uint4*>(const_cast<void*>(r_.s))[v0 + u * kThreads] = make_uint4(q[0], q[1], q[2], q[3]);
-        }
-      }
-    }
-    for (int i = n_vec * kPer + tid_; i < r_.n; i += kThreads) {
-      const float x = r_.load(i);
-      take(x);
-      if (i < r_.cap) {
-        if constexpr (F32)
-          static_cast<float*>(const_cast<void*>(r_.s))[i] = x;
-        else
-          static_cast<uint16_t*>(const_cast<void*>(r_.s))[i] = (uint16_t)(__float_as_uint(x) >> 16);
-      }
-    }
+      mn = fminf(mn, x);
+    });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -303,13 +410,18 @@ class Sampler {
       sh_.fmin[warp_] = mn;
     }
     __syncthreads();
-    if (tid_ == 0) {
-      for (int w = 1; w < kWarps; ++w) {
-        mx = fmaxf(mx, sh_.fmax[w]);
-        mn = fminf(mn, sh_.fmin[w]);
+    if (warp_ == 0) {
+      mx = lane_ < kWarps ? sh_.fmax[lane_] : -INFINITY;
+      mn = lane_ < kWarps ? sh_.fmin[lane_] : INFINITY;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
       }
-      sh_.top = mx;
-      sh_.low = mn;
+      if (lane_ == 0) {
+        sh_.top = mx;
+        sh_.low = mn;
+      }
     }
     cl_.sync();
     top_ = -INFINITY;
@@ -326,8 +438,7 @@ class Sampler {
   __device__ u64 sums(F f, u64* before) {
     u64 s = 0;
     each([&](float x, uint32_t i) { s += f(x, i); });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s = warp_sum64(s);
     if (lane_ == 0) sh_.wsum[warp_] = s;
     __syncthreads();
     u64 in_cta = 0, all = 0;
@@ -347,26 +458,22 @@ class Sampler {
     return z;
   }
 
-  // The entry at which the running sum of f first exceeds `target`: returned by one lane of
-  // the warp whose run holds it (after `sums` of the same f), -1 by every other thread.
+  // The entry of [i0, i1) at which the running sum of f, which is `before` at i0 and grows by
+  // `sum` over it, first exceeds `target`: returned by one lane of the warp that holds it, -1
+  // by every other thread.
   template <class F>
-  __device__ int find(F f, u64 before, u64 target) {
-    if (target < before || target >= before + sh_.wsum[warp_]) return -1;
-    for (int i0 = w0_; i0 < w1_; i0 += 64) {
+  __device__ int find(F f, u64 before, u64 target, int i0, int i1, u64 sum) {
+    if (target < before || target >= before + sum) return -1;
+    for (; i0 < i1; i0 += 64) {
       const int i = i0 + 2 * lane_;
       u64 wa = 0, wb = 0;
-      if (i < w1_) {
+      if (i < i1) {
         float x, y;
         r_.pair(i, x, y);
         wa = f(x, (uint32_t)(lo_ + i));
-        if (i + 1 < w1_) wb = f(y, (uint32_t)(lo_ + i + 1));
+        if (i + 1 < i1) wb = f(y, (uint32_t)(lo_ + i + 1));
       }
-      u64 inc = wa + wb;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane_ >= o) inc += v;
-      }
+      const u64 inc = warp_scan(wa + wb, lane_);
       const u64 step = __shfl_sync(0xffffffffu, inc, 31);
       if (target < before + step) {
         const u64 start = before + inc - wa - wb;
@@ -379,18 +486,477 @@ class Sampler {
     return -1;
   }
 
+  // Sums of weights by 32-bit atomics: three parts, each of fewer than 2^17 entries.
+  __device__ __forceinline__ static void add_parts(uint32_t (&part)[3][kWarps], int at, u64 w) {
+    constexpr uint32_t m = (1u << kPartBits) - 1u;
+    atomicAdd(&part[0][at], (uint32_t)w & m);
+    atomicAdd(&part[1][at], (uint32_t)(w >> kPartBits) & m);
+    atomicAdd(&part[2][at], (uint32_t)(w >> (2 * kPartBits)));
+  }
+  __device__ __forceinline__ static u64 parts(const uint32_t (&part)[3][kWarps], int at) {
+    return (u64)part[0][at] + ((u64)part[1][at] << kPartBits) + ((u64)part[2][at] << (2 * kPartBits));
+  }
+
+  // The first histogram (bin b holds the entries whose x is nearest to b * step; logits of
+  // few bits then lie in the middle of their bins, which the guess wants): top-k's border bin *bk with
+  // the entries before it and in it (unchanged where k entries outnumber those with a
+  // weight), and the bins [*lo, *hi] one of which holds top-p's border.
+  __device__ Borders borders(float per, float step, uint32_t k, float p) {
+    uint32_t* hist = sh_.f.hist;
+    for (int i = tid_; i < kFine / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    const float top = top_;
+    each([&](float x, uint32_t) {
+      const float v = fmaf(top - x, per, 0.5f);
+      if (v < (float)(kFine - 1)) atomicAdd(&hist[(int)v], 1u);  // what lies beyond has no weight
+    });
+    cl_.sync();
+    // Each CTA adds up its share of the bins over the cluster, in place (no other CTA reads
+    // that share of its histogram), and one CTA looks through the sums: with other rows' CTAs
+    // on the same SMs, what a cluster does twice costs time.
+    if (size_ > 1) {
+      const int share = kFine / 4 / size_;
+      for (int i = rank_ * share + tid_; i < (rank_ + 1) * share; i += kThreads) {
+        uint4 v[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < size_) v[r] = reinterpret_cast<const uint4*>(cl_.map_shared_rank(&sh_, r)->f.hist)[i];
+#pragma unroll
+        for (int r = 1; r < kMaxCluster; ++r)
+          if (r < size_) {
+            v[0].x += v[r].x;
+            v[0].y += v[r].y;
+            v[0].z += v[r].z;
+            v[0].w += v[r].w;
+          }
+        reinterpret_cast<uint4*>(hist)[i] = v[0];
+      }
+      cl_.sync();
+    }
+    if (rank_ == 0) look(step, k, p);
+    cl_.sync();
+    return cl_.map_shared_rank(&sh_, 0)->borders;
+  }
+
+  // The borders from the summed histogram, into this CTA's sh_.borders.
+  __device__ void look(float step, uint32_t k, float p) {
+    uint32_t c[kFinePer];
+#pragma unroll
+    for (int e = 0; e < kFinePer / 4; ++e) {
+      const int i = tid_ * (kFinePer / 4) + e;
+      const Shared* o = cl_.map_shared_rank(&sh_, i / (kFine / 4 / size_));
+      const uint4 v = reinterpret_cast<const uint4*>(o->f.hist)[i];
+      c[4 * e] = v.x;
+      c[4 * e + 1] = v.y;
+      c[4 * e + 2] = v.z;
+      c[4 * e + 3] = v.w;
+    }
+    if (tid_ == 0) {
+      sh_.borders = Borders{kFine - 1, 0u, 0u, 0, -1};
+      sh_.bins[0] = sh_.bins[1] = sh_.bins[2] = kFine - 2;
+      sh_.in_range[0] = sh_.in_range[1] = 0u;
+    }
+    uint32_t own = 0;
+#pragma unroll
+    for (int e = 0; e < kFinePer; ++e) own += c[e];
+    const uint32_t inc = warp_scan(own, lane_);
+    if (lane_ == 31) sh_.cwarp[warp_] = inc;
+    __syncthreads();
+    uint32_t before = inc - own;
+    for (int w = 0; w < warp_; ++w) before += sh_.cwarp[w];
+#pragma unroll
+    for (int e = 0; e < kFinePer; ++e) {
+      const int b = kFinePer * tid_ + e;
+      if (k > 0 && b < kFine - 1 && before < k && k <= before + c[e]) sh_.borders = Borders{b, before, c[e], 0, -1};
+      before += c[e];
+    }
+    __syncthreads();
+    const int bk = sh_.borders.bk;
+    const uint32_t above = sh_.borders.above;
+    if (p < 0.f) return;
+    // The weight of each bin's middle, times its entries that top-k leaves; the bin's largest
+    // and smallest are off from it by the same factors in every bin.
+    float v[kFinePer], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kFinePer; ++e) {
+      const int b = kFinePer * tid_ + e;
+      uint32_t cnt = b < bk ? c[e] : 0u;
+      if (b == bk && b < kFine - 1) cnt = k - above;
+      if (b == kFine - 1) cnt = 0u;
+      sum += (float)cnt * __expf(-(float)b * step);
+      v[e] = sum;
+    }
+    float pre = warp_scan(sum, lane_), all = 0.f;
+    if (lane_ == 31) sh_.fsum[warp_] = pre;
+    pre -= sum;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp_) pre += sh_.fsum[w];
+      all += sh_.fsum[w];
+    }
+    // The first bins whose running sums reach the goal: for certain in [bins[0], bins[1]]
+    // (widened by far more than the rounding of bins and sums), and most likely, by the
+    // middles, near bins[2]: their sums are off by the entries' places in their bins, which
+    // nearly average out.
+    const float off = __expf(step) * 1.0002f;
+    const float goal[3] = {p * all / off, p * all * off, p * all};
+    uint32_t first[3] = {kFine - 2, kFine - 2, kFine - 2};
+#pragma unroll
+    for (int e = kFinePer - 1; e >= 0; --e)
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (pre + v[e] >= goal[q]) first[q] = kFinePer * tid_ + e;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      first[q] = __reduce_min_sync(0xffffffffu, first[q]);
+      if (lane_ == 0 && first[q] < kFine - 2) atomicMin(&sh_.bins[q], first[q]);
+    }
+    __syncthreads();
+    // the widest of three ranges whose entries the list holds: the certain one where it is
+    // short, else two bins on either side of the likely one, or one
+    const int a = (int)sh_.bins[0], z = min((int)sh_.bins[1], bk), mid = (int)sh_.bins[2];
+    const int from[3] = {a, max(a, mid - 2), max(a, mid - 1)}, to[3] = {z, min(z, mid + 2), min(z, mid + 1)};
+    uint32_t in_range[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < kFinePer; ++e) {
+      const int b = kFinePer * tid_ + e;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (b >= from[q] && b <= to[q]) in_range[q] += c[e];
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      in_range[q] = __reduce_add_sync(0xffffffffu, in_range[q]);
+      if (lane_ == 0 && in_range[q]) atomicAdd(&sh_.in_range[q], in_range[q]);
+    }
+    __syncthreads();
+    const int q = sh_.in_range[0] <= kList / 4 ? 0 : sh_.in_range[1] <= kList - kList / 8 ? 1 : 2;
+    if (tid_ == 0) {
+      sh_.borders.lo = from[q];
+      sh_.borders.hi = to[q];
+    }
+  }
+
+  // Sorts v[0 .. n2) ascending, n2 a power of two of at least 64 and at most 2 * kThreads
+  // (bitonic). A warp holds 64 entries in registers, so that distances below 64 are shuffles
+  // and only the longer ones go through shared memory and the CTA's barrier.
+  __device__ void sort(u64* v, uint32_t n2) {
+    const uint32_t i = 64 * warp_ + lane_;  // this thread's entries: i and i + 32
+    const bool works = 64u * warp_ < n2;    // whole warps
+    u64 a = 0, b = 0;
+    if (works) {
+      a = v[i];
+      b = v[i + 32];
+    }
+    for (uint32_t k = 2; k <= n2; k *= 2) {
+      const bool up_a = (i & k) == 0, up_b = ((i + 32) & k) == 0;
+      for (uint32_t j = k / 2; j > 0; j /= 2) {
+        if (j >= 64) {
+          if (works) {
+            v[i] = a;
+            v[i + 32] = b;
+          }
+          __syncthreads();
+          if (works) {
+            const u64 x = v[i ^ j], y = v[(i + 32) ^ j];
+            const bool low = (i & j) == 0;
+            a = (a < x) == (low == up_a) ? a : x;
+            b = (b < y) == (low == up_b) ? b : y;
+          }
+          __syncthreads();
+        } else if (works) {
+          if (j == 32) {
+            if ((a > b) == up_a) {
+              const u64 x = a;
+              a = b;
+              b = x;
+            }
+          } else {
+            const u64 x = __shfl_xor_sync(0xffffffffu, a, j), y = __shfl_xor_sync(0xffffffffu, b, j);
+            const bool low = (lane_ & j) == 0;
+            a = (a < x) == (low == up_a) ? a : x;
+            b = (b < y) == (low == up_b) ? b : y;
+          }
+        }
+      }
+    }
+    if (works) {
+      v[i] = a;
+      v[i + 32] = b;
+    }
+    __syncthreads();
+  }
+
+  // Rank 0, after the cluster's sums and lists are there: the verdict, into its sh_.verdict.
+  __device__ void decide(const Borders& at, bool cut, bool nucleus, int k, float p, uint32_t least, float u) {
+    if (tid_ == 0) sh_.verdict.ok = 0;
+    u64 keep_all = 0, under = 0, rest = 0;
+    uint32_t n = 0, from[kMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      from[c] = n;
+      if (c < size_) {
+        const Shared* o = cl_.map_shared_rank(&sh_, c);
+        keep_all += o->tot[0];
+        under += o->tot[1];
+        rest += o->tot[2];
+        n += o->n_list;
+      }
+    }
+    if (n == 0 || n > (uint32_t)kList) return;
+    u64* v = reinterpret_cast<u64*>(sh_.f.hist);  // read by no other CTA any more
+    uint32_t n2 = 64;
+    while (n2 < n) n2 *= 2;
+    for (uint32_t j = tid_; j < n; j += kThreads) {
+      int c = 0;
+      uint32_t at_c = 0;
+#pragma unroll
+      for (int q = 1; q < kMaxCluster; ++q)
+        if (q < size_ && from[q] <= j) {
+          c = q;
+          at_c = from[q];
+        }
+      v[j] = cl_.map_shared_rank(&sh_, c)->f.list[j - at_c];
+    }
+    for (uint32_t j = n + tid_; j < n2; j += kThreads) v[j] = ~0ull;
+    __syncthreads();
+    sort(v, n2);
+    const uint32_t j0 = 2 * tid_;
+    u64 w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) w[e] = j0 + e < n ? weight(of_key(~(uint32_t)(v[j0 + e] >> 32))) : 0ull;
+    u64 before = warp_scan(w[0] + w[1], lane_);
+    if (lane_ == 31) sh_.scan[warp_] = before;
+    __syncthreads();
+    before -= w[0] + w[1];
+    for (int i = 0; i < warp_; ++i) before += sh_.scan[i];
+    // the list in order: top-p's bins, then top-k's border bin (the same, or a later one)
+    const uint32_t start_k = cut ? n - at.in : n;
+    const uint32_t end = cut ? start_k + ((uint32_t)k - at.above) : n;  // top-k keeps those before
+    const uint32_t lim = nucleus ? min(end, cut && at.hi < at.bk ? start_k : n) : end;
+    uint32_t m = end;
+    if (nucleus) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // weight before entries `end` and `lim` (both at most kList)
+        const u64 b = e ? before + w[0] : before;
+        if (j0 + e == end) sh_.last = b;
+        if (j0 + e == lim) sh_.before = b;
+      }
+      if (tid_ == kThreads - 1) {
+        if (end == kList) sh_.last = before + w[0] + w[1];
+        if (lim == kList) sh_.before = before + w[0] + w[1];
+      }
+      __syncthreads();
+      const u64 sure = keep_all + under, z = sure + rest + sh_.last;
+      const double g = ceil((double)p * (double)z);
+      const u64 goal = g >= 1.0 ? min((u64)g, z) : 1ull;
+      // the border lies inside the list, or it is not decided here
+      const bool inside = sure < goal && sure + sh_.before >= goal;
+      m = (uint32_t)__syncthreads_count(j0 < lim && sure + before < goal);
+      m += (uint32_t)__syncthreads_count(j0 + 1 < lim && sure + before + w[0] < goal);
+      if (!inside) return;
+    }
+    const u64 last = v[m - 1];  // m >= 1: k exceeds the entries above its bin, and sure < goal
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (j0 + e >= m) continue;
+      const u64 place = v[j0 + e];
+      if (~(uint32_t)(place >> 32) >= least) add_parts(sh_.cpart, (int)(uint32_t)place / a_.seg, w[e]);
+    }
+    __syncthreads();
+    if (tid_ == 0) {
+      u64 z = keep_all;
+      for (int c = 0; c < size_; ++c) z += parts(sh_.cpart, c);
+      Verdict o{last, target_of(u, z), 0, 1, 0};
+      u64 mine = cl_.map_shared_rank(&sh_, 0)->tot[0] + parts(sh_.cpart, 0);
+      while (o.owner < size_ - 1 && o.target >= o.pre + mine) {
+        o.pre += mine;
+        ++o.owner;
+        mine = cl_.map_shared_rank(&sh_, o.owner)->tot[0] + parts(sh_.cpart, o.owner);
+      }
+      sh_.verdict = o;
+    }
+  }
+
+  // The row's token, by way of the list; false where the list does not hold the border (then
+  // nothing is written). k = 0: no top-k; `least`: the least key that min-p keeps.
+  __device__ bool resolve(int k, float p, uint32_t least, float u) {
+    // infinite logits and temperatures beyond fp32's reciprocals have no finite x
+    if (top_ == INFINITY || !(inv_f_ > 0.f && inv_f_ < INFINITY)) return false;
+    const bool nucleus = p < 1.0f;
+    Borders at{kFine - 1, 0u, 0u, 0, -1};
+    float per = 0.f;
+    if (tid_ < 3 * kWarps) (&sh_.lpart[0][0])[tid_] = (&sh_.cpart[0][0])[tid_] = 0u;
+    if (tid_ == 0) sh_.n_list = 0u;
+    __syncthreads();
+    if (k > 0 || nucleus) {
+      const float range = (top_ - low_) * inv_f_;
+      float unit = (float)kFineUnit;  // finer bins where the row spans less than them all
+      for (int i = 0; i < 12 && range * unit * 2.0f <= (float)(kFine - 2); ++i) unit *= 2.0f;
+      per = inv_f_ * unit;
+      if (!(per < INFINITY)) return false;
+      at = borders(per, 1.0f / unit, (uint32_t)k, nucleus ? p : -1.0f);
+    }
+    const int bk = at.bk, lo = at.lo, hi = at.hi;
+    const bool cut = at.in > 0;  // top-k drops entries that have a weight
+    const bool any = nucleus || cut;
+    // Exact sums: kept for certain, above top-p's border but under min-p, and below the border
+    // (a thread's in fp64: at most 2^8 integers up to 2^43). An entry's bin is the whole part
+    // of v, so bins are told apart by v.
+    u64 s_keep = 0, s_under = 0, s_rest = 0;
+    const float least_f = least > 0u ? of_key(least) : -INFINITY, top = top_, inv_f = inv_f_;
+    double d_keep = 0.0, d_sure = 0.0, d_all = 0.0;
+    if (any) {
+      const float f_sure = (float)(nucleus ? lo : bk), f_lo = (float)lo, f_hi = (float)(hi + 1);
+      const float f_bk = (float)bk, f_cut = cut ? (float)(bk + 1) : 0.f;  // f_bk <= v < f_cut: top-k's border bin
+      const float f_end = nucleus ? f_bk : f_sure;                       // no weight is asked for from there on
+      // what is below all of them concerns nobody: with top-k alone, most of the row
+      const float f_last = fmaxf(fmaxf(f_end, f_hi), f_cut);
+      each_vector([&](float (&x)[kPer], uint32_t i) {
+        float v[kPer], least_v = INFINITY;
+        bool in_list = false;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          v[e] = fmaf(top - x[e], per, 0.5f);
+          least_v = fminf(least_v, v[e]);
+          in_list |= (v[e] >= f_lo && v[e] < f_hi) || (v[e] >= f_bk && v[e] < f_cut);
+        }
+        if (!(least_v < f_last)) return;
+        if (in_list) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            if ((v[e] >= f_lo && v[e] < f_hi) || (v[e] >= f_bk && v[e] < f_cut)) {
+              const uint32_t to = atomicAdd(&sh_.n_list, 1u);
+              if (to < kList) sh_.f.list[to] = place_of(key_of(x[e]), i + e);
+              v[e] = INFINITY;  // its weight is added up later
+            }
+        }
+        if (!(least_v < f_end)) return;
+        if (nucleus) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const double w = weight_in(x[e], (top - x[e]) * inv_f);
+            add_below(d_all, w, v[e], f_end);
+            add_below(d_sure, w, v[e], f_sure);
+            add_below(d_keep, w, v[e], f_sure, x[e], least_f);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            if (v[e] < f_sure) add_below(d_keep, weight_in(x[e], (top - x[e]) * inv_f), v[e], f_sure, x[e], least_f);
+        }
+      });
+      s_rest = (u64)(d_all - d_sure);
+      s_under = (u64)(d_sure - d_keep);
+    } else {
+      each_vector([&](float (&x)[kPer], uint32_t) {
+        float most = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) most = fmaxf(most, x[e]);
+        if (!(most >= least_f)) return;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const float xf = (top - x[e]) * inv_f;
+          add_below(d_keep, weight_in(x[e], xf), xf, kMaxX, x[e], least_f);
+        }
+      });
+    }
+    s_keep = (u64)d_keep;
+    if (!nucleus) s_under = 0;
+    s_keep = warp_sum64(s_keep);
+    s_under = warp_sum64(s_under);
+    s_rest = warp_sum64(s_rest);
+    if (lane_ == 0) {
+      sh_.ws[0][warp_] = s_keep;
+      sh_.ws[1][warp_] = s_under;
+      sh_.ws[2][warp_] = s_rest;
+    }
+    __syncthreads();
+    if (warp_ < 3) {
+      const u64 v = warp_sum64(lane_ < kWarps ? sh_.ws[warp_][lane_] : 0ull);
+      if (lane_ == 0) sh_.tot[warp_] = v;
+    }
+    cl_.sync();
+    Verdict o{~0ull, 0, 0, 1, 0};
+    if (any) {
+      if (rank_ == 0) decide(at, cut, nucleus, k, p, least, u);
+      cl_.sync();
+      o = cl_.map_shared_rank(&sh_, 0)->verdict;
+      if (!o.ok) return false;
+    } else {
+      u64 tot[kMaxCluster], z = 0;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        tot[c] = c < size_ ? cl_.map_shared_rank(&sh_, c)->tot[0] : 0ull;
+        z += tot[c];
+      }
+      o.target = target_of(u, z);
+      u64 pre = 0;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        if (o.target >= pre && o.target < pre + tot[c]) {
+          o.owner = c;
+          o.pre = pre;
+        }
+        pre += tot[c];
+      }
+    }
+    if (o.owner != rank_) return true;
+    if (any) {
+      // the list's kept weights by run of this CTA
+      for (uint32_t j = tid_; j < sh_.n_list; j += kThreads) {
+        const u64 place = sh_.f.list[j];
+        const uint32_t key = ~(uint32_t)(place >> 32);
+        if (place <= o.last && key >= least) add_parts(sh_.lpart, ((int)(uint32_t)place - lo_) / run_, weight(of_key(key)));
+      }
+      __syncthreads();
+    }
+    u64 pre = o.pre;
+    const u64 target = o.target, last = o.last;
+    int w = 0;
+    u64 run = sh_.ws[0][0] + parts(sh_.lpart, 0);
+    while (w < kWarps - 1 && target >= pre + run) {
+      pre += run;
+      ++w;
+      run = sh_.ws[0][w] + parts(sh_.lpart, w);
+    }
+    // that warp's run, weighed again by all warps
+    const int r0 = min(r_.n, w * run_), r1 = min(r_.n, r0 + run_);
+    const int sub = (run_ / 64 + kWarps - 1) / kWarps * 64;
+    const int i0 = min(r1, r0 + warp_ * sub), i1 = min(r1, i0 + sub);
+    auto kept = [this, last, least](float x, uint32_t i) {
+      const uint32_t key = key_of(x);
+      return key >= least && place_of(key, i) <= last ? weight(x) : 0ull;
+    };
+    u64 s = 0;
+    for (int i = i0 + 2 * lane_; i < i1; i += 64) {
+      float x, y;
+      r_.pair(i, x, y);
+      s += kept(x, (uint32_t)(lo_ + i));
+      if (i + 1 < i1) s += kept(y, (uint32_t)(lo_ + i + 1));
+    }
+    s = warp_sum64(s);
+    if (lane_ == 0) sh_.scan[warp_] = s;
+    __syncthreads();
+    for (int i = 0; i < warp_; ++i) pre += sh_.scan[i];
+    const int i = find(kept, pre, target, i0, i1, s);
+    if (i >= 0) a_.out[row_id_] = i;
+    return true;
+  }
+
   // Adds the CTAs' histograms, and finds the bin b with (measure of the bins before it)
   // < goal <= (that and its own); bin 0 holds the largest keys. MASS: the goal is
   // p * total, fixed here at the first level. False: the row's measure is below the goal.
   template <bool MASS>
   __device__ bool border(bool first, double p, u64* goal) {
     __syncthreads();
-    u64 h = sh_.part[0][tid_];
-    if (MASS) h += ((u64)sh_.part[1][tid_] << kPartBits) + ((u64)sh_.part[2][tid_] << (2 * kPartBits));
-    sh_.hist[tid_] = h;
+    u64 h = sh_.s.part[0][tid_];
+    if (MASS) h += ((u64)sh_.s.part[1][tid_] << kPartBits) + ((u64)sh_.s.part[2][tid_] << (2 * kPartBits));
+    sh_.s.hist[tid_] = h;
     cl_.sync();
     h = 0;
-    for (int c = 0; c < size_; ++c) h += cl_.map_shared_rank(&sh_, c)->hist[tid_];
+    for (int c = 0; c < size_; ++c) h += cl_.map_shared_rank(&sh_, c)->s.hist[tid_];
     u64 inc = h;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -419,24 +985,24 @@ class Sampler {
   }
 
   __device__ __forceinline__ void clear() {
-    sh_.part[0][tid_] = 0u;
-    sh_.part[1][tid_] = 0u;
-    sh_.part[2][tid_] = 0u;
+    sh_.s.part[0][tid_] = 0u;
+    sh_.s.part[1][tid_] = 0u;
+    sh_.s.part[2][tid_] = 0u;
     __syncthreads();
   }
 
   template <bool MASS>
   __device__ __forceinline__ void count(uint32_t bin, float x) {
     if (MASS) {
-      const u64 w = weight_of(exponent(x));
+      const u64 w = weight_any(x);
       if (w == 0ull) return;
       constexpr uint32_t m = (1u << kPartBits) - 1u;
       const uint32_t a = (uint32_t)w & m, b = (uint32_t)(w >> kPartBits) & m, c = (uint32_t)(w >> (2 * kPartBits));
-      if (a) atomicAdd(&sh_.part[0][bin], a);
-      if (b) atomicAdd(&sh_.part[1][bin], b);
-      if (c) atomicAdd(&sh_.part[2][bin], c);
+      if (a) atomicAdd(&sh_.s.part[0][bin], a);
+      if (b) atomicAdd(&sh_.s.part[1][bin], b);
+      if (c) atomicAdd(&sh_.s.part[2][bin], c);
     } else {
-      atomicAdd(&sh_.part[0][bin], 1u);
+      atomicAdd(&sh_.s.part[0][bin], 1u);
     }
   }
 
@@ -453,7 +1019,7 @@ class Sampler {
     };
     clear();
     each([&](float x, uint32_t i) {
-      if (keep.has(key_of(x), i)) count<MASS>((uint32_t)bin_of(x), x);
+      if (keep.has(order_key(x), i)) count<MASS>((uint32_t)bin_of(x), x);
     });
     if (!border<MASS>(true, p, &goal)) return keep;
     // the border bin's keys: listed aside where they fit, and their range
@@ -466,10 +1032,10 @@ class Sampler {
     }
     __syncthreads();
     each([&](float x, uint32_t i) {
-      const uint32_t k = key_of(x);
+      const uint32_t k = order_key(x);
       if (bin_of(x) == b0 && keep.has(k, i)) {
         const uint32_t at = atomicAdd(&sh_.n_list, 1u);
-        if (at < kList) sh_.list[at] = k;
+        if (at < kList) sh_.s.list[at] = k;
         atomicMin(&sh_.kmin, k);
         atomicMax(&sh_.kmax, k);
       }
@@ -490,12 +1056,12 @@ class Sampler {
       clear();
       if (n_list <= kList) {
         for (uint32_t j = tid_; j < n_list; j += kThreads) {
-          const uint32_t k = sh_.list[j];
+          const uint32_t k = sh_.s.list[j];
           if (k >= k0 && k <= k1) count<MASS>((k1 - k) >> shift, of_key(k));
         }
       } else {
         each([&](float x, uint32_t i) {
-          const uint32_t k = key_of(x);
+          const uint32_t k = order_key(x);
           if (k >= k0 && k <= k1 && keep.has(k, i)) count<MASS>((k1 - k) >> shift, x);
         });
       }
@@ -508,17 +1074,17 @@ class Sampler {
       k0 = k1 - k0 > width ? k1 - width : k0;
     }
     // of the entries with key k1: the first m, in index order
-    const u64 each_w = MASS ? weight_of(exponent(of_key(k1))) : 1ull;
+    const u64 each_w = MASS ? weight_any(of_key(k1)) : 1ull;
     const u64 m = (goal - above + each_w - 1) / each_w, c = sh_.inside / each_w;
     Keep out{k1, k1 == keep.key ? keep.index : 0xffffffffu};
     if (m < c) {
       auto same = [keep, k1](float x, uint32_t i) {
-        const uint32_t k = key_of(x);
+        const uint32_t k = order_key(x);
         return k == k1 && keep.has(k, i) ? 1ull : 0ull;
       };
       u64 before;
       sums(same, &before);
-      const int i = find(same, before, m - 1);
+      const int i = find(same, before, m - 1, w0_, w1_, sh_.wsum[warp_]);
       if (i >= 0)
         for (int o = 0; o < size_; ++o) cl_.map_shared_rank(&sh_, o)->cut = (uint32_t)i;
       cl_.sync();
@@ -529,7 +1095,7 @@ class Sampler {
 };
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Shared& sh = *reinterpret_cast<Shared*>(smem + kDataBytes);
@@ -605,7 +1171,7 @@ int check_sample(const void* logits, int64_t row_stride, const float* uniform, c
 template <bool F32>
 int launch_sample(const SampleArgs& a, int64_t rows, int cluster, cudaStream_t st) {
   constexpr int smem = kDataBytes + (int)sizeof(Shared);
-  static_assert(smem <= 232448, "shared memory");
+  static_assert(2 * (smem + 1024) <= 233472, "two CTAs an SM");
   if (cudaFuncSetAttribute(sample_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return LS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -642,10 +1208,10 @@ int run_sample(const void* logits, int64_t row_stride, const float* uniform, con
   a.V = vocab;
   a.cap = cap;
   a.vec = (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 && (row_stride * elt) % 16 == 0 ? 1 : 0;
-  // the fewest CTAs whose shared memory holds the row; more while the rows leave SMs idle
+  // the fewest CTAs whose shared memory holds the row; more while the rows leave places idle
   int cluster = 1;
   while (cluster < kMaxCluster && (vocab + cluster - 1) / cluster > std::min(cap, kMaxSeg) - 8) cluster *= 2;
-  while (cluster < kMaxCluster && rows * cluster * 2 <= 148 && vocab / cluster >= 8192) cluster *= 2;
+  while (cluster < kMaxCluster && rows * cluster * 2 <= 2 * 148 && vocab / cluster >= 4096) cluster *= 2;
   a.seg = ((vocab + cluster - 1) / cluster + 7) / 8 * 8;
   (void)cudaGetLastError();
   return f32 ? launch_sample<true>(a, rows, cluster, st) : launch_sample<false>(a, rows, cluster, st);

@@ -27,38 +27,44 @@ from .binding import LS_OK, LSError, TreeOpts, load_library, make_dims
 __all__ = ["KVCacheQ8", "VerifyAttnQ8", "CrossAttnQ8", "sample", "tree_accept_sample"]
 
 SCALE_BLOCKS = (16, 32, 64, 128)
+CODE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _tensor(t, name: str, dtypes, device=None):
-    """A dense CUDA tensor of one of `dtypes` on `device`, or an error that names it."""
+def _refuse(t, name: str, dtypes, device, shape):
+    """Raises the error that says what of `t` does not fit."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
-        raise TypeError(f"{name} must be {dtypes}, got {t.dtype}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _shape(t, name: str, *shape):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-
-
-def _ints(t, name: str, device, *shape):
-    _tensor(t, name, torch.int32, device)
-    _shape(t, name, *shape)
+def _ptr(t, name: str, dtype, device, shape=None):
+    """The address of a dense CUDA tensor of this dtype, device and shape, or an error that
+    names it. (One test on the way that every call takes: small calls are bound by it.)"""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or not t.is_contiguous()
+            or shape is not None and t.shape != shape):
+        _refuse(t, name, (dtype,), device, shape)
     return t.data_ptr()
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _call(device, what: str, fn, *args):
     """fn(*args, stream) on `device` and its current stream; raises what it returns."""
-    with torch.cuda.device(device):
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
     if rc != LS_OK:
         raise LSError(rc, what)
 
@@ -73,21 +79,21 @@ class KVCacheQ8:
     """
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale, page_table):
-        codes = (torch.float8_e4m3fn, torch.uint8)
-        _tensor(k_pages, "k_pages", codes)
-        if k_pages.dim() != 4:
-            raise ValueError("k_pages must be [num_pages, page_size, H_kv, d]")
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if not isinstance(t, torch.Tensor) or t.dtype not in CODE_DTYPES or not t.is_cuda or not t.is_contiguous():
+                _refuse(t, name, CODE_DTYPES, None, None)
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be [num_pages, page_size, H_kv, d]")
         self.device = k_pages.device
         self.num_pages, self.page_size, self.num_kv_heads, self.head_dim = map(int, k_pages.shape)
-        _tensor(v_pages, "v_pages", codes, self.device)
-        _shape(v_pages, "v_pages", *k_pages.shape)
-        _tensor(k_scale, "k_scale", torch.float32, self.device)
+        if v_pages.device != self.device or v_pages.shape != k_pages.shape:
+            _refuse(v_pages, "v_pages", CODE_DTYPES, self.device, k_pages.shape)
+        _ptr(k_scale, "k_scale", torch.float32, self.device)
         if k_scale.dim() != 3 or k_scale.shape[1] < 1 or self.page_size % k_scale.shape[1]:
             raise ValueError("k_scale must be [num_pages, page_size // scale_block, H_kv]")
-        _shape(k_scale, "k_scale", self.num_pages, k_scale.shape[1], self.num_kv_heads)
-        _tensor(v_scale, "v_scale", torch.float32, self.device)
-        _shape(v_scale, "v_scale", *k_scale.shape)
-        _tensor(page_table, "page_table", torch.int32, self.device)
+        _ptr(k_scale, "k_scale", torch.float32, self.device, (self.num_pages, k_scale.shape[1], self.num_kv_heads))
+        _ptr(v_scale, "v_scale", torch.float32, self.device, k_scale.shape)
+        _ptr(page_table, "page_table", torch.int32, self.device)
         if page_table.dim() != 2:
             raise ValueError("page_table must be [B, max_pages_per_seq]")
         self.scale_block = self.page_size // int(k_scale.shape[1])
@@ -122,24 +128,24 @@ class KVCacheQ8:
         return ctypes.byref(self._dims[tree_size])
 
     def _rows(self, k, v, names):
-        _tensor(k, names[0], torch.bfloat16, self.device)
-        _tensor(v, names[1], torch.bfloat16, self.device)
-        if k.dim() != 3 or tuple(k.shape[1:]) != (self.num_kv_heads, self.head_dim):
-            raise ValueError(f"{names[0]} must be [rows, {self.num_kv_heads}, {self.head_dim}], got {tuple(k.shape)}")
-        _shape(v, names[1], *k.shape)
-        return k.data_ptr(), v.data_ptr()
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError(f"{names[0]} must be a tensor [rows, {self.num_kv_heads}, {self.head_dim}]")
+        shape = (k.shape[0], self.num_kv_heads, self.head_dim)
+        return (_ptr(k, names[0], torch.bfloat16, self.device, shape),
+                _ptr(v, names[1], torch.bfloat16, self.device, shape))
 
     def append(self, k_new, v_new, cu_seqlens, cu_new, max_new: int, *, cu_seqlens_out=None):
         """Rows cu_new[b]:cu_new[b+1] of k_new / v_new (bf16 [rows, H_kv, d]) become the next
         tokens of sequence b, at most max_new of them. Returns the new cu_seqlens
         (cu_seqlens_out, or a new tensor; never cu_seqlens itself)."""
         k, v = self._rows(k_new, v_new, ("k_new", "v_new"))
-        cu = _ints(cu_seqlens, "cu_seqlens", self.device, self.batch + 1)
-        new = _ints(cu_new, "cu_new", self.device, self.batch + 1)
+        ends = (self.batch + 1,)
+        cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, self.device, ends)
+        new = _ptr(cu_new, "cu_new", torch.int32, self.device, ends)
         if cu_seqlens_out is None:
             cu_seqlens_out = torch.empty_like(cu_seqlens)
-        out = _ints(cu_seqlens_out, "cu_seqlens_out", self.device, self.batch + 1)
-        _call(self.device, "ls_kv_append_q8", load_library().ls_kv_append_q8, k, v, new, int(k_new.shape[0]),
+        out = _ptr(cu_seqlens_out, "cu_seqlens_out", torch.int32, self.device, ends)
+        _call(self.device, "ls_kv_append_q8", load_library().ls_kv_append_q8, k, v, new, k_new.shape[0],
               int(max_new), cu, out, self._ref, self._write_dims(1))
         return cu_seqlens_out
 
@@ -149,22 +155,23 @@ class KVCacheQ8:
         as the acceptance calls return it; trees are packed by cu_tree, or T nodes each.
         Returns the new cu_seqlens."""
         k, v = self._rows(k_tree, v_tree, ("k_tree", "v_tree"))
-        cu = _ints(cu_seqlens, "cu_seqlens", self.device, self.batch + 1)
-        length = _ints(accept_len, "accept_len", self.device, self.batch)
-        _tensor(accept_path, "accept_path", torch.int32, self.device)
+        ends = (self.batch + 1,)
+        cu = _ptr(cu_seqlens, "cu_seqlens", torch.int32, self.device, ends)
+        length = _ptr(accept_len, "accept_len", torch.int32, self.device, (self.batch,))
+        path = _ptr(accept_path, "accept_path", torch.int32, self.device)
         if accept_path.dim() != 2 or accept_path.shape[0] != self.batch:
             raise ValueError(f"accept_path must be [{self.batch}, T]")
-        size, nodes = int(accept_path.shape[1]), int(k_tree.shape[0])
+        size, nodes = accept_path.shape[1], k_tree.shape[0]
         trees = None
         if cu_tree is not None:
-            trees = _ints(cu_tree, "cu_tree", self.device, self.batch + 1)
+            trees = _ptr(cu_tree, "cu_tree", torch.int32, self.device, ends)
         elif nodes != self.batch * size:
             raise ValueError(f"k_tree must have {self.batch} * {size} rows, got {nodes}")
         if cu_seqlens_out is None:
             cu_seqlens_out = torch.empty_like(cu_seqlens)
-        out = _ints(cu_seqlens_out, "cu_seqlens_out", self.device, self.batch + 1)
-        _call(self.device, "ls_kv_commit_q8", load_library().ls_kv_commit_q8, k, v, trees, nodes, length,
-              accept_path.data_ptr(), cu, out, self._ref, self._write_dims(size))
+        out = _ptr(cu_seqlens_out, "cu_seqlens_out", torch.int32, self.device, ends)
+        _call(self.device, "ls_kv_commit_q8", load_library().ls_kv_commit_q8, k, v, trees, nodes, length, path, cu, out,
+              self._ref, self._write_dims(size))
         return cu_seqlens_out
 
 
@@ -192,31 +199,27 @@ class _AttnQ8:
         if self.ws_bytes == 0:
             raise LSError(1, f"{self._name}_workspace_size returned 0 (invalid or unsupported dims)")
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+        self._ws_ptr = self.workspace.data_ptr()
 
     def _check(self, q, cache, cu_seqlens, out, lse):
+        """(rows, q, cu_seqlens, out, lse addresses, out, lse)"""
         d = self.dims
         if not isinstance(cache, KVCacheQ8):
             raise TypeError("cache must be a KVCacheQ8")
         if (cache.batch, cache.num_kv_heads, cache.head_dim) != (d.batch, d.num_kv_heads, d.head_dim):
             raise ValueError("the cache's batch, kv heads or head dimension are not the call's")
-        if cache.device != self.device:
-            raise ValueError(f"the cache is on {cache.device}, the call on {self.device}")
-        self._rows = d.batch * d.tree_size
-        if self.tree is not None and self.tree.cu_tree:
-            self._rows = self.tree.total_nodes
-        _tensor(q, "q", torch.bfloat16, self.device)
-        _shape(q, "q", self._rows, d.num_q_heads, d.head_dim)
+        dev = self.device
+        if cache.device != dev:
+            raise ValueError(f"the cache is on {cache.device}, the call on {dev}")
+        rows = self.tree.total_nodes if self.tree is not None and self.tree.cu_tree else d.batch * d.tree_size
+        shape = (rows, d.num_q_heads, d.head_dim)
+        qp = _ptr(q, "q", torch.bfloat16, dev, shape)
         if out is None:
             out = torch.empty_like(q)
-        else:
-            _tensor(out, "out", torch.bfloat16, self.device)
-            _shape(out, "out", *q.shape)
         if lse is None:
-            lse = torch.empty(self._rows, d.num_q_heads, dtype=torch.float32, device=self.device)
-        else:
-            _tensor(lse, "lse", torch.float32, self.device)
-            _shape(lse, "lse", self._rows, d.num_q_heads)
-        return _ints(cu_seqlens, "cu_seqlens", self.device, d.batch + 1), out, lse
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+        return (rows, qp, _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev, (d.batch + 1,)),
+                _ptr(out, "out", torch.bfloat16, dev, shape), _ptr(lse, "lse", torch.float32, dev, shape[:2]), out, lse)
 
     def check(self) -> int:
         """Waits for the current stream; the device status of the last call (binding.STATUS_NAMES)."""
@@ -238,15 +241,12 @@ class VerifyAttnQ8(_AttnQ8):
         return int(load_library().ls_verify_attn_q8_workspace_size(self._dims_ref, self._tree_ref))
 
     def __call__(self, q, cache, k_tree, v_tree, parent, cu_seqlens, out=None, lse=None):
-        cu, out, lse = self._check(q, cache, cu_seqlens, out, lse)
-        d = self.dims
-        for t, name in ((k_tree, "k_tree"), (v_tree, "v_tree")):
-            _tensor(t, name, torch.bfloat16, self.device)
-            _shape(t, name, self._rows, d.num_kv_heads, d.head_dim)
-        par = _ints(parent, "tree_parent", self.device, self._rows)
-        _call(self.device, self._name, load_library().ls_verify_attn_q8, q.data_ptr(), cache._ref, k_tree.data_ptr(),
-              v_tree.data_ptr(), par, cu, self._tree_ref, out.data_ptr(), lse.data_ptr(), self._dims_ref,
-              self.workspace.data_ptr(), self.ws_bytes)
+        rows, qp, cu, op, lp, out, lse = self._check(q, cache, cu_seqlens, out, lse)
+        dev, shape = self.device, (rows, self.dims.num_kv_heads, self.dims.head_dim)
+        _call(dev, self._name, load_library().ls_verify_attn_q8, qp, cache._ref,
+              _ptr(k_tree, "k_tree", torch.bfloat16, dev, shape), _ptr(v_tree, "v_tree", torch.bfloat16, dev, shape),
+              _ptr(parent, "tree_parent", torch.int32, dev, (rows,)), cu, self._tree_ref, op, lp, self._dims_ref,
+              self._ws_ptr, self.ws_bytes)
         return out, lse
 
 
@@ -265,29 +265,32 @@ class CrossAttnQ8(_AttnQ8):
         return int(load_library().ls_cross_attn_q8_workspace_size(self._dims_ref))
 
     def __call__(self, q, cache, cu_seqlens, out=None, lse=None):
-        cu, out, lse = self._check(q, cache, cu_seqlens, out, lse)
-        _call(self.device, self._name, load_library().ls_cross_attn_q8, q.data_ptr(), cache._ref, cu, out.data_ptr(),
-              lse.data_ptr(), self._dims_ref, self.workspace.data_ptr(), self.ws_bytes)
+        _, qp, cu, op, lp, out, lse = self._check(q, cache, cu_seqlens, out, lse)
+        _call(self.device, self._name, load_library().ls_cross_attn_q8, qp, cache._ref, cu, op, lp, self._dims_ref,
+              self._ws_ptr, self.ws_bytes)
         return out, lse
 
 
+_KINDS = {torch.float32: binding.LS_DTYPE_F32, torch.bfloat16: binding.LS_DTYPE_BF16}
+
+
 def _sampling(logits, uniform, temperature, top_k, top_p, min_p, dense: bool):
-    """(rows, vocab, row stride, dtype, options and what they keep alive) of checked logits."""
-    if not isinstance(logits, torch.Tensor):
-        raise TypeError("logits must be a torch tensor")
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    if not logits.is_cuda:
-        raise ValueError("logits must be on a CUDA device")
-    if logits.dim() != 2 or logits.shape[1] < 1:
+    """(rows, vocab, row stride, uniform's address, dtype, options and what they keep alive)"""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _KINDS or not logits.is_cuda:
+        _refuse(logits, "logits", tuple(_KINDS), None, None)
+    shape = logits.shape
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError("logits must be [rows, vocab]")
-    rows, vocab = map(int, logits.shape)
-    stride = int(logits.stride(0)) if rows > 1 else vocab
-    if vocab > 1 and logits.stride(1) != 1 or stride < vocab or dense and not logits.is_contiguous():
-        raise ValueError("logits must be contiguous" if dense else "logits must have contiguous, disjoint rows")
-    dev = logits.device
-    _tensor(uniform, "uniform", torch.float32, dev)
-    _shape(uniform, "uniform", rows)
+    rows, vocab = shape
+    stride = vocab
+    if not logits.is_contiguous():
+        stride, inner = logits.stride()
+        if rows < 2:
+            stride = vocab
+        if dense or vocab > 1 and inner != 1 or stride < vocab:
+            raise ValueError("logits must be contiguous" if dense else "logits must have contiguous, disjoint rows")
+    dev, per_row = logits.device, (rows,)
+    u = _ptr(uniform, "uniform", torch.float32, dev, per_row)
     keep, ptrs = [], []
     for value, name, dtype in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
                                (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
@@ -295,13 +298,10 @@ def _sampling(logits, uniform, temperature, top_k, top_p, min_p, dense: bool):
             ptrs.append(None)
             continue
         if isinstance(value, (int, float)):  # one value for every row
-            value = torch.full((rows,), value, dtype=dtype, device=dev)
-        _tensor(value, name, dtype, dev)
-        _shape(value, name, rows)
-        keep.append(value)
-        ptrs.append(value.data_ptr())
-    kind = binding.LS_DTYPE_F32 if logits.dtype == torch.float32 else binding.LS_DTYPE_BF16
-    return rows, vocab, stride, kind, binding.SampleOpts(*ptrs), keep
+            value = torch.full(per_row, value, dtype=dtype, device=dev)
+            keep.append(value)
+        ptrs.append(_ptr(value, name, dtype, dev, per_row))
+    return rows, vocab, stride, u, _KINDS[logits.dtype], binding.SampleOpts(*ptrs), keep
 
 
 def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
@@ -310,13 +310,12 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
     tensor with one per row (fp32; top_k int32), or None (1, off, off, off); temperature 0 is
     greedy. The order of the filters and the draw are those of ``ls_sample``. Returns int32
     [rows]."""
-    rows, vocab, stride, kind, opts, keep = _sampling(logits, uniform, temperature, top_k, top_p, min_p, False)
+    rows, vocab, stride, u, kind, opts, keep = _sampling(logits, uniform, temperature, top_k, top_p, min_p, False)
     dev = logits.device
     if out is None:
-        out = torch.empty(rows, dtype=torch.int32, device=dev)
-    _ints(out, "out", dev, rows)
-    _call(dev, "ls_sample", load_library().ls_sample, logits.data_ptr(), stride, uniform.data_ptr(),
-          ctypes.byref(opts), out.data_ptr(), rows, vocab, kind)
+        out = torch.empty((rows,), dtype=torch.int32, device=dev)
+    _call(dev, "ls_sample", load_library().ls_sample, logits.data_ptr(), stride, u, ctypes.byref(opts),
+          _ptr(out, "out", torch.int32, dev, (rows,)), rows, vocab, kind)
     return out
 
 
@@ -327,27 +326,28 @@ def tree_accept_sample(logits, uniform, tree_tokens, tree_parent, tree_size: int
     per node; trees of tree_size nodes each, or packed by cu_tree int32 [B+1] with at most
     tree_size nodes. Returns (node_token [N], accept_len [B], accept_path [B, tree_size],
     next_token [B]), int32."""
-    rows, vocab, _, kind, opts, keep = _sampling(logits, uniform, temperature, top_k, top_p, min_p, True)
+    rows, vocab, _, u, kind, opts, keep = _sampling(logits, uniform, temperature, top_k, top_p, min_p, True)
     dev = logits.device
     if tree_size < 1:
         raise ValueError("tree_size must be positive")
     trees = None
     if cu_tree is not None:
-        _tensor(cu_tree, "cu_tree", torch.int32, dev)
+        trees = _ptr(cu_tree, "cu_tree", torch.int32, dev)
         if cu_tree.dim() != 1 or cu_tree.shape[0] < 2:
             raise ValueError("cu_tree must be [B + 1]")
-        batch, trees = int(cu_tree.shape[0]) - 1, cu_tree.data_ptr()
+        batch = cu_tree.shape[0] - 1
     else:
         batch = rows // tree_size
         if batch < 1 or batch * tree_size != rows:
             raise ValueError(f"{rows} rows of logits are not whole trees of {tree_size} nodes")
-    tok = _ints(tree_tokens, "tree_tokens", dev, rows)
-    par = _ints(tree_parent, "tree_parent", dev, rows)
-    node_token = torch.empty(rows, dtype=torch.int32, device=dev)
-    accept_path = torch.empty(batch, tree_size, dtype=torch.int32, device=dev)
-    accept_len, next_token = torch.empty(2, batch, dtype=torch.int32, device=dev)
+    tok = _ptr(tree_tokens, "tree_tokens", torch.int32, dev, (rows,))
+    par = _ptr(tree_parent, "tree_parent", torch.int32, dev, (rows,))
+    # one allocation for the four results
+    node_token, accept_len, accept_path, next_token = torch.empty(
+        (rows + 2 * batch + batch * tree_size,), dtype=torch.int32, device=dev).split(
+        (rows, batch, batch * tree_size, batch))
     dims = binding.AcceptDims(batch, tree_size, vocab, kind)
-    _call(dev, "ls_tree_accept_sample", load_library().ls_tree_accept_sample, logits.data_ptr(), uniform.data_ptr(),
+    _call(dev, "ls_tree_accept_sample", load_library().ls_tree_accept_sample, logits.data_ptr(), u,
           ctypes.byref(opts), tok, par, trees, rows, node_token.data_ptr(), accept_len.data_ptr(),
           accept_path.data_ptr(), next_token.data_ptr(), ctypes.byref(dims))
-    return node_token, accept_len, accept_path, next_token
+    return node_token, accept_len, accept_path.view(batch, tree_size), next_token
