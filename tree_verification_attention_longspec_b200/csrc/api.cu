@@ -424,12 +424,12 @@ namespace {
 
 // ---- the 8-bit cache
 
-// Rows of a unit: 8 where a kv head's rows fit them, else 16 (several units a head where
-// they do not fit those).
+// The kernel for a kv head's rows: up to 16 stream through registers, in units of 8 or 16
+// rows; more go to the tensor cores' 128-row tiles (0).
 int32_t q8_slot_rows(const ls_verify_dims* d) {
   if (d == nullptr || d->num_kv_heads < 1) return 8;  // make_plan refuses it
   const long long rows = (long long)d->tree_size * (d->num_q_heads / d->num_kv_heads);
-  return rows <= 8 ? 8 : 16;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 0;
 }
 
 int q8_plan(const ls_verify_dims* d, Plan* p, bool with_tree, const ls_tree_opts* tree) {
@@ -524,7 +524,7 @@ int run_q8(const void* q, const ls_kv_q8* kv, const void* k_tree, const void* v_
     a.k_tree = ra.k_rot;
     a.after_prep = 1;
   }
-  if (ls::launch_q8_rows(a, st) != cudaSuccess) return LS_ERR_CUDA;
+  if ((p.slot_rows > 0 ? ls::launch_q8_rows(a, st) : ls::launch_q8_tc(a, st)) != cudaSuccess) return LS_ERR_CUDA;
   return run_combine(cu_seqlens, out, lse, dims, workspace, workspace_bytes, stream, with_tree, tree, &p);
 }
 

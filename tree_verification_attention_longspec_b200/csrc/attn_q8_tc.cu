@@ -1,0 +1,971 @@
+// Attention partials over the 8-bit cache on the 5th-generation tensor cores.
+//
+// The computation, the work split and the partials are partials_tc.cu's: one CTA per chunk,
+// a 256-row unit as two 128-row query tiles in ping-pong (or, for a unit of at most 128
+// rows, both tiles on its rows and alternate key blocks), S_t and O_t in TMEM, P over the
+// scores, the tree block last. What the 8-bit cache changes:
+//
+// Operands. tcgen05 takes both operands of a product in one type. The codes are exact in
+// f16, so K and V become f16 tiles in shared memory, Q becomes f16 in place (each row times
+// a power of two that brings its largest element to [2^14, 2^15): exact down to 2^-29 of
+// it), and so do the tree block's keys and values (a power of two for each of the two
+// tiles). P is f16 too: 11 bits where bf16 has 8.
+// Scales. A score is s * ck + lv in the log2 domain, ck the key block's scale times the
+// softmax scale over the row's power of two, lv = log2 of the value scale; both are constant
+// over 16 keys (no scale block is shorter), so they cost one multiplier and one addend a
+// group. P = 2^(s * ck + lv - m + kOff) then carries the value scale, the product needs
+// none, and the row's sum takes it out again, 1 / vs a group. m is the running maximum of
+// s * ck + lv, raised when exceeded by kRaise, so P stays below 2^15.
+//
+// Warp roles (384 threads, one CTA per SM):
+//   warps 0-3, 4-7  softmax of tile 0, of tile 1
+//   warp 8          TMA producer: Q, then the blocks' codes (page by page) into a raw ring
+//   warp 9          MMA issuer
+//   warps 10, 11    converters: raw tile -> swizzled f16 tile (cvt.f16x2.e4m3x2, two codes an
+//                   instruction; rows past the sequence become zeros, so that whatever they
+//                   hold meets weight 0 as 0), the block's scales into a table, and the
+//                   tree's keys and values from global memory
+// Converting in two warps costs the issue slots of ~700 instructions a warp and block, next
+// to the softmax's ~1000 a warp; reading 8-bit K and V by the tensor core itself would
+// need Q and P in 8 bits, P with them.
+// Every wait is bounded; on a timeout the CTA raises an abort flag, all roles drain their
+// in-flight copies and MMAs, TMEM is freed, and the chunk status reports it.
+#include <cudaTypedefs.h>
+
+#include "q8_device.cuh"
+#include "sm100.cuh"
+
+namespace ls {
+namespace {
+using namespace sm100;
+
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kConvertWarp = 10;  // and 11
+constexpr int kConverters = 64;   // threads
+constexpr int kTiles = 2;         // 128-row query tiles per CTA
+constexpr int kHalf = 64;         // keys per P half
+constexpr int kGroup = 16;        // keys that share their scales for certain
+constexpr int kGroups = kBlockN / kGroup;
+constexpr int kTables = 8;  // scale tables in flight: a block's is written after the softmax of the eighth before it
+constexpr uint64_t kDrainNs = 4000000000ull;
+constexpr float kRaise = 6.0f;  // log2 units that a score may exceed the running maximum by
+constexpr float kOff = 9.0f;    // so P stays below 2^15
+static_assert(kUnitRows == kTiles * 128, "a unit is two 128-row tiles");
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kPanelBytes = 128 * 128;             // 128 rows x 64 f16, 128B-swizzled
+  static constexpr int kTileBytes = kPanels * kPanelBytes;  // 128 rows x D f16
+  static constexpr int kRawBytes = 128 * D;                 // 128 rows x D codes
+  static constexpr int kSlots = D == 128 ? 3 : 6;           // f16 tiles
+  static constexpr int kRaw = D == 128 ? 4 : 8;             // raw tiles
+  // Q: [panel][kUnitRows rows][128 B]; tile t is rows [128 t, 128 t + 128) of each panel
+  static constexpr int kQPanelBytes = kUnitRows * 128;
+  static constexpr int kQOff = 0;
+  static constexpr int kSlotOff = kPanels * kQPanelBytes;
+  static constexpr int kRawOff = kSlotOff + kSlots * kTileBytes;
+  static constexpr int kBarOff = kRawOff + kRaw * kRawBytes;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS = 0;    // S_t / P_t at 128 t
+  static constexpr uint32_t kColO = 256;  // O_t at 256 + D t
+  static_assert(kPanels * kQPanelBytes >= 128 * D * 4 && kSlots * kTileBytes >= 128 * D * 4, "epilogue staging");
+};
+
+struct alignas(64) TcParams {
+  CUtensorMap tmap_q;
+  CUtensorMap tmap_k;  // codes
+  CUtensorMap tmap_v;
+  CUtensorMap tmap_o;  // o_part as [n_chunks * 256 rows][d] fp32, stores of 128 rows x 32 floats
+  Q8Args a;
+};
+
+struct Bars {
+  uint64_t q_full;                      // the unit's Q rows are in shared memory (bf16)
+  uint64_t raw_full[8], raw_empty[8];   // raw tiles
+  uint64_t full[6], empty[6];           // f16 tiles
+  uint64_t table_full[kTables];         // a block's scales
+  uint64_t s_full[kTiles];              // S_t(j) is in TMEM (and O_t holds every PV before it)
+  uint64_t p_full[kTiles][2];           // half h of P_t(j) is in TMEM
+  uint64_t o_full[kTiles];              // every MMA of tile t finished
+  uint32_t tmem_base;
+  uint32_t abort;
+  uint32_t tree_err;                    // a parent link that is not a rooted tree's
+  float kc[kTables][kGroups];           // key scales of the block's groups
+  float lv[kTables][kGroups];           // log2 of the value scales
+  float rv[kTables][kGroups];           // 1 / value scale
+  int8_t q_shift[kUnitRows];            // log2 of the row's power of two
+  int16_t parent[kMaxTree];             // the sequence's tree (chunks that hold the tree block)
+};
+static_assert(Cfg<128>::kRaw <= 8 && Cfg<64>::kRaw <= 8 && Cfg<128>::kSlots <= 6 && Cfg<64>::kSlots <= 6, "barriers");
+
+// The dynamic window of a CTA less 1 KB; the layout is aligned up to 1024 bytes inside it
+// (the 128-byte swizzle atom repeats every 1024 bytes).
+constexpr int kSmemWindow = 232448;
+template <int D>
+constexpr int smem_need() {
+  return Cfg<D>::kBarOff + (int)sizeof(Bars) + 1024;
+}
+static_assert(smem_need<128>() <= kSmemWindow && smem_need<64>() <= kSmemWindow, "shared memory");
+
+// Instruction descriptor for kind::f16 with f16 A/B and an fp32 accumulator.
+constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4)                                 // D: f32 (A, B: f16 = 0)
+         | ((b_mn_major ? 1u : 0u) << 16)          // B major-ness (A is K-major)
+         | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
+         | (static_cast<uint32_t>(M >> 4) << 24);  // M / 16
+}
+
+// AND of `pred` over the `n` threads that meet at named barrier `id`.
+__device__ __forceinline__ bool bar_and(uint32_t id, uint32_t n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// Waits only on time (used to drain in-flight work after an abort).
+__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t never = 0;
+  return mbar_wait_bounded(bar, parity, &never, kDrainNs);
+}
+
+// P for 64 scores of four groups: 2^(s * ck + cm), packed to f16 pairs; adds each group's
+// sum, times rv, to l. A masked score (-inf) gives 0.
+__device__ __forceinline__ void make_p(const float (&s)[kHalf], const float* ck, const float* cm, const float* rv,
+                                       uint32_t (&pk)[kHalf / 2], float& l) {
+#pragma unroll
+  for (int g = 0; g < kHalf / kGroup; ++g) {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int e = g * kGroup / 2; e < (g + 1) * kGroup / 2; ++e) {
+      float x0, x1;
+      fma2_bc(x0, x1, s[2 * e], s[2 * e + 1], ck[g], cm[g]);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      add2(s0, s1, p0, p1);
+      pk[e] = pack_f16x2(p0, p1);
+    }
+    l = fmaf(s0 + s1, rv[g], l);
+  }
+}
+
+// Tree mask (LongSpec, gist.science summary, section 2C, "Baum-Maskierung") on the
+// scores of the tree block in this thread's TMEM lane: key x (tree node x) stays visible
+// when x is the row's node or one of its ancestors, found by following parent links.
+// Every link is checked (node 0 is the root with parent -1, any other node's parent
+// lies below it), so the walk ends; a failed check raises `bad`. node < 0 (a padding
+// row) masks every key. The scores go back to TMEM as -inf where masked.
+__device__ __forceinline__ bool mask_tree_scores(const int16_t* parent, uint32_t tS, int node) {
+  uint32_t am[4] = {0u, 0u, 0u, 0u};
+  bool bad = false;
+  if (node >= 0) {
+    int x = node;
+    for (int step = 0; step <= kMaxTree; ++step) {
+      const uint32_t bit = 1u << (x & 31);
+      const int w = x >> 5;
+      am[0] |= w == 0 ? bit : 0u;
+      am[1] |= w == 1 ? bit : 0u;
+      am[2] |= w == 2 ? bit : 0u;
+      am[3] |= w == 3 ? bit : 0u;
+      const int pp = parent[x];
+      if (x == 0) {
+        bad = pp != -1;
+        break;
+      }
+      if (pp < 0 || pp >= x) {
+        bad = true;
+        break;
+      }
+      x = pp;
+    }
+  }
+  __syncwarp();  // the TMEM accesses below are warp-collective
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t r[32];
+    tmem_ld32(tS + 32 * q, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!((am[q] >> e) & 1u)) r[e] = __float_as_uint(-INFINITY);
+    tmem_st32(tS + 32 * q, r);
+  }
+  tmem_wait_st();
+  return bad;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constant__ TcParams P) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOff);
+  const Q8Args& a = P.a;
+  const Plan& p = a.p;
+  const KvQ8& kv = a.kv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t wait_ns = (uint64_t)p.wait_ns;  // limit of every bounded wait below
+
+  const int32_t* cu = plan_cu(p, a.cu);  // kernel parameters when the host gave lengths
+  const ChunkCoord c = locate_chunk(p, cu, blockIdx.x);
+  if (!c.valid) return;  // more CTAs than the device lengths need: the combine reports it
+  const int n_keys = c.key_end - c.key_begin;
+  const int nb = (n_keys + kBlockN - 1) / kBlockN;     // prefix blocks
+  const int tail_end = n_keys - (nb - 1) * kBlockN;    // keys of the last one
+  const bool has_tree = c.has_tree;
+  const int nbt = nb + (has_tree ? 1 : 0);  // blocks, the tree block (block nb) last
+  const int seq_len = cu[c.b + 1] - cu[c.b];
+  // sliding window: a row at depth d sees the attended keys from window_cut(d) on, which
+  // is below 2 * 128, so only the chunks that start there cut rows individually
+  const bool win_rows = p.window > 0 && nb > 0 && c.key_begin < 2 * kBlockN;
+  int tree_base, tree_n;  // the sequence's tree nodes (none if cu_tree is bad: the combine reports it)
+  tree_range(p, a.cu_tree, c.b, &tree_base, &tree_n);
+  const int tok0 = c.rgi * p.tpu;                         // first tree node of the unit
+  const int rows_here = min(p.tpu, tree_n - tok0) * p.g;  // rows of the unit that exist
+  const bool alt = unit_alternates(rows_here);            // both tiles on these rows
+  if (rows_here <= 0) {  // a unit past the sequence's tree: nothing to attend for
+    if (tid == 0) a.chunk_status[blockIdx.x] = 0u;
+    return;
+  }
+  if (nbt == 0) {  // empty key range: an empty partial (two of them when the tiles alternate)
+    for (int r = tid; r < rows_here; r += kThreads) {
+      a.lse_part[(size_t)blockIdx.x * kUnitRows + r] = -INFINITY;
+      if (alt) a.lse_part[(size_t)blockIdx.x * kUnitRows + 128 + r] = -INFINITY;
+    }
+    if (tid == 0) a.chunk_status[blockIdx.x] = 0u;
+    return;
+  }
+  volatile uint32_t* abort = &bars->abort;
+
+  // The tiles in the order that the MMA thread uses them: K(j), V(j) for j = 0, 1, ...; with
+  // alternate blocks K(0), K(1), then V(j) and K(j + 2) for j = 0, 1, ... (no K past the
+  // last block).
+  const int n_tiles = 2 * nbt;
+  const int pro = nbt < 2 ? nbt : 2, pairs = nbt > 2 ? nbt - 2 : 0;
+  auto tile_of = [&](int ld, int* j, int* val) {
+    if (!alt) {
+      *j = ld >> 1;
+      *val = ld & 1;
+    } else if (ld < pro) {
+      *j = ld;
+      *val = 0;
+    } else if (ld - pro < 2 * pairs) {
+      const int r = ld - pro;
+      *j = (r >> 1) + ((r & 1) ? 2 : 0);
+      *val = (r & 1) ? 0 : 1;
+    } else {
+      *j = pairs + (ld - pro - 2 * pairs);
+      *val = 1;
+    }
+  };
+  // When the tree kernel writes q and k_tree (rotated), this grid may start before that grid
+  // ends: the prefix loads go ahead, Q and the tree block wait for it.
+  auto wait_prior = [&]() {
+    if (a.after_prep) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
+
+  if (warp == kProducerWarp && lane == 0) {
+    mbar_init(&bars->q_full, 1);
+    for (int s = 0; s < C::kRaw; ++s) {
+      mbar_init(&bars->raw_full[s], 1);
+      mbar_init(&bars->raw_empty[s], 2);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&bars->full[s], 2);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int s = 0; s < kTables; ++s) mbar_init(&bars->table_full[s], 1);
+    for (int t = 0; t < kTiles; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t][0], 128);
+      mbar_init(&bars->p_full[t][1], 128);
+      mbar_init(&bars->o_full[t], 1);
+    }
+    bars->abort = 0u;
+    bars->tree_err = 0u;
+    fence_mbar_init();
+    tma_prefetch_map(&P.tmap_q);
+    tma_prefetch_map(&P.tmap_k);
+    tma_prefetch_map(&P.tmap_v);
+    tma_prefetch_map(&P.tmap_o);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tbase = bars->tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------------ TMA producer
+    // a box is bh rows (a page, or 128 rows of a larger one); lane l issues box l of a block
+    const int bh = kv.page_size < kBlockN ? kv.page_size : kBlockN;
+    const int n_boxes = kBlockN / bh;
+    const int n_pages = (seq_len + kv.page_size - 1) / kv.page_size;
+    int issued = 0, slot = 0, use = 0;
+    bool ok = true;
+    if (lane == 0 && !a.after_prep) {
+      mbar_arrive_expect_tx(&bars->q_full, C::kPanels * 128 * p.g * p.tpu);
+#pragma unroll
+      for (int pn = 0; pn < C::kPanels; ++pn)
+        tma_load_4d(smem + C::kQOff + pn * C::kQPanelBytes, &P.tmap_q, &bars->q_full, pn * 64, 0, c.kh, tree_base + tok0);
+    }
+    bool q_issued = !a.after_prep;
+    for (int ld = 0; ld < n_tiles && ok; ++ld) {
+      if (!q_issued && (ld == 2 || issued > 0)) {
+        // the first tile is on its way: now Q, once the tree kernel has written it
+        wait_prior();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full, C::kPanels * 128 * p.g * p.tpu);
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_4d(smem + C::kQOff + pn * C::kQPanelBytes, &P.tmap_q, &bars->q_full, pn * 64, 0, c.kh, tree_base + tok0);
+        }
+        q_issued = true;
+      }
+      int j, val;
+      tile_of(ld, &j, &val);
+      if (j == nb) continue;  // the tree block comes through the converters
+      // this lane's page box; a table entry is only a TMA coordinate, so a bad one reads zeros
+      // or another page; boxes past the sequence end read its last page (made zeros later)
+      int prow = 0;
+      if (lane < n_boxes) {
+        const int key = c.key_skip + c.key_begin + j * kBlockN + lane * bh;
+        int lp = key / kv.page_size;
+        if (lp >= n_pages) lp = n_pages - 1;
+        if (lp >= kv.max_pages) lp = kv.max_pages - 1;
+        const int32_t page = kv.page_table[(size_t)c.b * kv.max_pages + lp];
+        prow = ((uint32_t)page < (uint32_t)kv.num_pages ? page : 0) * kv.page_size + key % kv.page_size;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->raw_empty[slot], (use & 1) ^ 1, abort, wait_ns));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[slot], C::kRawBytes);
+      __syncwarp();
+      if (lane < n_boxes)
+        tma_load_3d(smem + C::kRawOff + slot * C::kRawBytes + lane * bh * D, val ? &P.tmap_v : &P.tmap_k,
+                    &bars->raw_full[slot], 0, c.kh, prow);
+      ++issued;
+      if (++slot == C::kRaw) {
+        slot = 0;
+        ++use;
+      }
+    }
+    if (!q_issued) {  // no prefix tile at all
+      wait_prior();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars->q_full, C::kPanels * 128 * p.g * p.tpu);
+#pragma unroll
+        for (int pn = 0; pn < C::kPanels; ++pn)
+          tma_load_4d(smem + C::kQOff + pn * C::kQPanelBytes, &P.tmap_q, &bars->q_full, pn * 64, 0, c.kh, tree_base + tok0);
+      }
+    }
+    // make sure no copy is still writing shared memory when the CTA ends
+    if (lane == 0) {
+      drain_wait(&bars->q_full, 0);
+      const int first = issued > C::kRaw ? issued - C::kRaw : 0;
+      for (int seq = first; seq < issued; ++seq) drain_wait(&bars->raw_full[seq % C::kRaw], (seq / C::kRaw) & 1);
+    }
+    __syncwarp();
+  } else if (warp >= kConvertWarp) {
+    // ------------------------------------------------------------------ converters
+    const int ct = tid - kConvertWarp * 32;  // 0 .. 63
+    // a block's scales: lane g of the first warp holds group g's, read one block ahead
+    float ks = 1.f, vs = 1.f;
+    auto read_scales = [&](int j) {
+      const int key = c.key_begin + j * kBlockN + lane * kGroup;
+      ks = vs = 1.f;
+      if (lane < kGroups && key < c.key_end) {
+        const size_t at = (size_t)(q8_row(kv, c.b, c.key_skip + key) / kv.scale_block) * p.Hkv + c.kh;
+        ks = __ldg(kv.k_scale + at);
+        vs = __ldg(kv.v_scale + at);
+      }
+    };
+    auto write_scales = [&](int j, float k, float lv, float rv) {
+      if (lane < kGroups) {
+        bars->kc[j % kTables][lane] = k;
+        bars->lv[j % kTables][lane] = lv;
+        bars->rv[j % kTables][lane] = rv;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->table_full[j % kTables]);
+    };
+    const bool first_warp = warp == kConvertWarp;
+    if (first_warp) read_scales(0);
+    int slot = 0, use = 0, raw = 0, raw_use = 0;
+    bool ok = true;
+    for (int ld = 0; ld < n_tiles && ok; ++ld) {
+      int j, val;
+      tile_of(ld, &j, &val);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->empty[slot], (use & 1) ^ 1, abort, wait_ns));
+      if (!ok) break;
+      uint8_t* dst = smem + C::kSlotOff + slot * C::kTileBytes;
+      if (j < nb) {
+        if (first_warp && !val) {  // its scales, before any score of it exists
+          const float v = fminf(fmaxf(vs, 8.6736174e-19f), 1.8446744e19f);
+          write_scales(j, fmaxf(ks, 1.17549435e-38f), log2f(v), 1.f / v);
+          if (j + 1 < nb) read_scales(j + 1);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->raw_full[raw], raw_use & 1, abort, wait_ns));
+        if (!ok) break;
+        const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
+        const int lim = j == nb - 1 ? tail_end : kBlockN;
+        constexpr int kChunks = D / 16;  // 16-byte chunks of a raw row
+        constexpr int kIter = 128 * kChunks / kConverters;
+        constexpr int kBatch = 8;
+#pragma unroll
+        for (int it = 0; it < kIter; it += kBatch) {
+          uint4 w[kBatch];
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) w[e] = *reinterpret_cast<const uint4*>(src + (ct + (it + e) * kConverters) * 16);
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e) {
+            const int i = ct + (it + e) * kConverters;
+            const int row = i / kChunks, cc = i % kChunks;
+            if (row >= lim) w[e] = make_uint4(0u, 0u, 0u, 0u);
+            uint4 x, y;
+            x.x = e4m3x2_f16x2(w[e].x);
+            x.y = e4m3x2_f16x2_hi(w[e].x);
+            x.z = e4m3x2_f16x2(w[e].y);
+            x.w = e4m3x2_f16x2_hi(w[e].y);
+            y.x = e4m3x2_f16x2(w[e].z);
+            y.y = e4m3x2_f16x2_hi(w[e].z);
+            y.z = e4m3x2_f16x2(w[e].w);
+            y.w = e4m3x2_f16x2_hi(w[e].w);
+            // chunk q of a panel row sits at q ^ (row & 7); the upper panel's lanes store their
+            // second half first, so that a row's eight lanes cover all eight bank groups
+            uint8_t* line = dst + (cc / 4) * C::kPanelBytes + row * 128;
+            const int q0 = 2 * (cc % 4), sw = row & 7;
+            const bool flip = cc >= 4;
+            *reinterpret_cast<uint4*>(line + (((q0 + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? y : x;
+            *reinterpret_cast<uint4*>(line + (((q0 + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? x : y;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->raw_empty[raw]);
+        if (++raw == C::kRaw) {
+          raw = 0;
+          ++raw_use;
+        }
+      } else {
+        // The tree block: bf16 rows from global memory, times a power of two for the tile.
+        // Each warp finds the tile's largest magnitude by itself (no barrier between two warps
+        // of which one may have given up).
+        constexpr int kChunks = D / 8;  // 16-byte chunks of a bf16 row
+        const size_t stride = (size_t)p.Hkv * D, head = ((size_t)tree_base * p.Hkv + c.kh) * D;
+        if (!val) wait_prior();
+        auto largest = [&](const uint16_t* from) {
+          float amax = 0.f;
+          for (int i = lane; i < tree_n * kChunks; i += 32) {
+            const uint4 w = *reinterpret_cast<const uint4*>(from + (size_t)(i / kChunks) * stride + (i % kChunks) * 8);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          return amax;
+        };
+        auto value_shift = [&]() {
+          return min(max(f16_shift(largest(a.v_tree + head)), -kMaxScaleExp), -kMinScaleExp);
+        };
+        const uint16_t* from = (val ? a.v_tree : a.k_tree) + head;
+        const int sh = val ? value_shift() : f16_shift(largest(from));
+        if (first_warp && !val) {  // the block's table: all groups alike
+          const int vsh = value_shift();
+          write_scales(j, pow2f(-sh), (float)-vsh, pow2f(vsh));
+        }
+        const float mul = pow2f(sh);
+        for (int i = ct; i < 128 * kChunks; i += kConverters) {
+          const int row = i / kChunks, cc = i % kChunks;
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (row < tree_n) w = *reinterpret_cast<const uint4*>(from + (size_t)row * stride + cc * 8);
+          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * mul, __uint_as_float(u[e] & 0xffff0000u) * mul);
+          *reinterpret_cast<uint4*>(dst + (cc / 8) * C::kPanelBytes + row * 128 + (((cc % 8) ^ (row & 7)) << 4)) =
+              make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+      fence_proxy_async_smem();  // the tile is read by the tensor core
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->full[slot]);
+      if (++slot == C::kSlots) {
+        slot = 0;
+        ++use;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ Q to f16 (warps 0-7)
+    // Thread r converts row r of the unit in place: 16-byte chunks of the row, in an order
+    // that starts at the lane, so that a warp's accesses spread over the banks. The rows
+    // after the box's tpu * g become zeros, so that no stale shared memory enters an MMA.
+    if (warp < 8) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->q_full, 0, abort, wait_ns));
+      if (got) {
+        const bool row_there = tid < p.tpu * p.g;
+        uint8_t* line = smem + C::kQOff + tid * 128;
+        float amax = 0.f;
+        if (row_there) {
+#pragma unroll 4
+          for (int i = 0; i < C::kPanels * 8; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(line + (i / 8) * C::kQPanelBytes + (((i + lane) & 7) << 4));
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+          }
+        }
+        const int sh = f16_shift(amax);
+        const float mul = pow2f(sh);
+        bars->q_shift[tid] = (int8_t)sh;
+#pragma unroll 4
+        for (int i = 0; i < C::kPanels * 8; ++i) {
+          uint4* at = reinterpret_cast<uint4*>(line + (i / 8) * C::kQPanelBytes + (((i + lane) & 7) << 4));
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (row_there) w = *at;
+          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * mul, __uint_as_float(u[e] & 0xffff0000u) * mul);
+          *at = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      // the tree of the sequence, for the tree mask; a parent outside [-1, T) is stored
+      // as a value that fails the walk's checks
+      if (has_tree || win_rows) {
+        for (int x = tid; x < tree_n; x += 256) {
+          const int32_t pp = a.parent[(size_t)tree_base + x];
+          bars->parent[x] = (int16_t)(pp >= -1 && pp < tree_n ? pp : kMaxTree);
+        }
+      }
+    }
+    // Q and the tree are in shared memory: warps 0-7 and the MMA warp meet at barrier 1
+    asm volatile("bar.sync 1, 288;" ::: "memory");
+
+    if (warp == kMmaWarp) {
+      if (lane == 0) {
+        // -------------------------------------------------------------- MMA issuer
+        constexpr uint32_t idesc_qk = umma_idesc_f16(128, kBlockN, false);
+        constexpr uint32_t idesc_pv = umma_idesc_f16(128, D, true);
+        // A descriptor differs from another of the same kind only in its start-address
+        // field (address >> 4 in the low 14 bits; shared addresses stay below 256 KB, so
+        // adding an offset never carries out of it): build the bases once, add offsets.
+        const uint64_t dq0 = umma_sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
+        constexpr uint32_t kQPanel16 = C::kQPanelBytes >> 4, kQTile16 = (128 * 128) >> 4;
+        const uint64_t dk0 = umma_sdesc_sw128(smem_u32(smem + C::kSlotOff), 16, 1024);
+        const uint64_t dv0 = umma_sdesc_sw128(smem_u32(smem + C::kSlotOff), C::kPanelBytes, 1024);
+        constexpr uint32_t kTile16 = C::kTileBytes >> 4, kPanel16 = C::kPanelBytes >> 4;
+        // S_t = Q_t K^T into tile t's score buffer; K sits in ring slot `slot`
+        auto issue_qk = [&](int t, int slot) {
+          const uint64_t dq = dq0 + (uint64_t)((alt ? 0 : t) * kQTile16);  // both tiles read tile 0's Q rows when alternating
+          const uint64_t dk = dk0 + (uint64_t)(slot * kTile16);
+          const uint32_t tS = tbase + C::kColS + t * kBlockN;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t koff = (kk & 3) * 2;  // 32 bytes per K step inside a panel (16-byte units)
+            umma_ss(tS, dq + (kk >> 2) * kQPanel16 + koff, dk + (kk >> 2) * kPanel16 + koff, idesc_qk,
+                    kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bars->s_full[t]);
+        };
+        // O_t += P_t V over keys [64h, 64h+64) of block j: four K = 16 steps, P from TMEM
+        auto issue_pv = [&](int t, int slot, int j, int h) {
+          const uint64_t dv = dv0 + (uint64_t)(slot * kTile16);
+          const uint32_t tP = tbase + C::kColS + t * kBlockN;
+          const uint32_t tO = tbase + C::kColO + t * D;
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int kk = 4 * h + k4;
+            umma_ts(tO, tP + kk * 8, dv + kk * (2048 / 16), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+        };
+        // P written by the softmax warps' tcgen05.st: their wait::st, fence and arrive pair
+        // with this wait and the fence after it before an MMA reads P
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          const bool got = mbar_wait_bounded(bar, parity, abort, wait_ns);
+          if (got) tc_fence_after_sync();
+          return got;
+        };
+        // K, V written by the converters, whose proxy fence precedes their arrival
+        auto wait_tile = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort, wait_ns); };
+        int slot = 0, use = 0;  // ring position of the next tile, in consumption order
+        auto advance = [&]() {
+          if (++slot == C::kSlots) {
+            slot = 0;
+            use ^= 1;
+          }
+        };
+        bool ok = true;
+        if (alt) {
+          // alternate blocks: tile t takes blocks t, t + 2, ...; S_t = Q K(t)^T first, then
+          // for j = 0, 1, ...: PV of block j for tile j % 2 and that tile's next QK^T
+          for (int t = 0; t < kTiles && t < nbt && ok; ++t) {
+            ok = wait_tile(&bars->full[slot], use);
+            if (!ok) break;
+            issue_qk(t, slot);
+            umma_commit(&bars->empty[slot]);
+            advance();
+          }
+          for (int j = 0; j < nbt && ok; ++j) {
+            const int t = j & 1, i = j >> 1;  // tile and its own block count
+            ok = wait_tile(&bars->full[slot], use);  // V(j)
+            if (!ok) break;
+            const int sv = slot;
+            advance();
+            ok = wait(&bars->p_full[t][0], i & 1);
+            if (!ok) break;
+            issue_pv(t, sv, i, 0);
+            ok = wait(&bars->p_full[t][1], i & 1);
+            if (!ok) break;
+            issue_pv(t, sv, i, 1);
+            umma_commit(&bars->empty[sv]);
+            if (j + 2 < nbt) {
+              ok = wait_tile(&bars->full[slot], use);  // K(j + 2)
+              if (!ok) break;
+              issue_qk(t, slot);
+              umma_commit(&bars->empty[slot]);
+              advance();
+            } else if (t == 0) {
+              umma_commit(&bars->o_full[0]);  // tile 0's last PV; no QK^T follows it
+            }
+          }
+        }
+        if (ok && !alt) {
+          ok = wait_tile(&bars->full[slot], use);  // K(0)
+          if (ok) {
+            issue_qk(0, slot);
+            issue_qk(1, slot);
+            umma_commit(&bars->empty[slot]);
+            advance();
+          }
+        }
+        for (int j = 0; j < nbt && ok && !alt; ++j) {
+          const int sv = slot, uv = use;  // V(j)
+          advance();
+          const bool more = j + 1 < nbt;
+          const int sk = slot, uk = use;  // K(j+1), when there is one
+          const uint32_t pp = j & 1;
+          ok = wait_tile(&bars->full[sv], uv);
+          for (int t = 0; t < kTiles && ok; ++t) {
+            ok = wait(&bars->p_full[t][0], pp);
+            if (!ok) break;
+            issue_pv(t, sv, j, 0);
+            ok = wait(&bars->p_full[t][1], pp);
+            if (!ok) break;
+            issue_pv(t, sv, j, 1);
+            // V(j) is free once both tiles' PV have read it: released before the next QK^T,
+            // so that its refill (a few microseconds in flight) starts that much earlier
+            if (t == 1) umma_commit(&bars->empty[sv]);
+            if (!more && t == 0) umma_commit(&bars->o_full[0]);  // tile 0's epilogue may start
+            if (more) {
+              if (t == 0) ok = wait_tile(&bars->full[sk], uk);
+              if (!ok) break;
+              issue_qk(t, sk);
+            }
+          }
+          if (!ok) break;
+          if (more) {
+            umma_commit(&bars->empty[sk]);
+            advance();
+          }
+        }
+        // tile 0's last PV precedes tile 1's in issue order, so o_full[1] completes last
+        umma_commit(&bars->o_full[1]);
+        drain_wait(&bars->o_full[1], 0);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- softmax / epilogue
+      const int t = warp >> 2;                 // query tile
+      const int row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t tS = tbase + lane_base + C::kColS + t * kBlockN;
+      const uint32_t tO = tbase + lane_base + C::kColO + t * D;
+      float m = -INFINITY, l = 0.f;  // running maximum (log2 units) of this row, its sum of weights
+      const int ur = alt ? row : t * 128 + row;  // row of the unit (both tiles' rows when alternating)
+      const bool has_row = ur < rows_here;
+      const float cs = p.scale_log2 * pow2f(-(int)bars->q_shift[ur]);
+      const int node = tok0 + ur / p.g;   // its tree node
+      int cut = 0;                        // window: first attended key this row sees
+      if (win_rows && has_row) {
+        int x = node, depth = 0;
+        for (int step = 0; step < kMaxTree && x > 0; ++step) {
+          const int pp = bars->parent[x];
+          if (pp < 0 || pp >= x) break;  // not a rooted tree: the tree block's chunk reports it
+          x = pp;
+          ++depth;
+        }
+        cut = window_cut(p, seq_len, depth);
+      }
+      bool ok = true;
+      // blocks of this tile: all of them, or every other one (from block t) when alternating
+      const int n_mine = alt ? (nbt - t + 1) / 2 : nbt;
+      for (int i = 0; i < n_mine; ++i) {
+        const int j = alt ? 2 * i + t : i;  // the block
+        const int tb = j % kTables;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->table_full[tb], (j / kTables) & 1, abort, wait_ns) &&
+                                         mbar_wait_bounded(&bars->s_full[t], i & 1, abort, wait_ns));
+        if (!ok) break;
+        tc_fence_after_sync();
+        int shift = 0;  // masked leading columns (this row)
+        if (win_rows && j < nb) shift = max(0, min(cut - (c.key_begin + j * kBlockN), kBlockN));
+        const int lim = j == nb - 1 ? tail_end : kBlockN;  // columns from here on are masked
+        const bool tree_blk = j == nb;                      // keys = the sequence's tree nodes
+        if (tree_blk && mask_tree_scores(bars->parent, tS, has_row ? node : -1)) bars->tree_err = 1u;
+        // All 128 scores for the row maximum, kept in registers for both halves of P (P
+        // goes to columns 0..63, whose scores are in registers by then; d = 64 reads keys
+        // 64..127 again below).
+        float lo[kHalf];
+        float hi[kHalf];
+        float ck[kGroups], cm[kGroups];
+        float mx = -INFINITY;
+        {
+          uint32_t r[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, r[q]);
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            // not 0 (a row or a block of zeros), so that a masked score stays -inf
+            ck[g] = fmaxf(bars->kc[tb][g] * cs, 1.17549435e-38f);
+            cm[g] = bars->lv[tb][g];
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < kHalf; ++e) {
+            lo[e] = __uint_as_float(r[e >> 5][e & 31]);
+            hi[e] = __uint_as_float(r[2 + (e >> 5)][e & 31]);
+          }
+          if (shift > 0 || lim < kBlockN) {  // the sequence's last prefix block, or a window's first
+#pragma unroll
+            for (int e = 0; e < kHalf; ++e) {
+              if (e < shift || e >= lim) lo[e] = -INFINITY;
+              if (e + kHalf < shift || e + kHalf >= lim) hi[e] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < kGroups / 2; ++g) {
+            float m0 = lo[16 * g], m1 = hi[16 * g];
+#pragma unroll
+            for (int e = 1; e < 15; e += 2) {
+              m0 = fmax3(m0, lo[16 * g + e], lo[16 * g + e + 1]);
+              m1 = fmax3(m1, hi[16 * g + e], hi[16 * g + e + 1]);
+            }
+            m0 = fmaxf(m0, lo[16 * g + 15]);
+            m1 = fmaxf(m1, hi[16 * g + 15]);
+            mx = fmax3(mx, fmaf(m0, ck[g], cm[g]), fmaf(m1, ck[g + 4], cm[g + 4]));
+          }
+        }
+        const bool raise = mx > m + kRaise;
+        const bool any_raise = __any_sync(0xffffffffu, raise);
+        const float m_new = raise ? mx : m;
+        // a row that has seen no visible key yet (a padding row of a tree-only chunk)
+        // keeps m = -inf; its P is 0 against any finite reference
+        const float m_off = (m_new == -INFINITY ? 0.f : m_new) - kOff;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) cm[g] -= m_off;
+        if (any_raise) {
+          // the maximum moved up: rescale what O_t and l hold. O_t is idle: every PV of
+          // this tile issued before S_t(j) has completed (s_full), and PV_t(j) waits for
+          // this warpgroup's P. f = 1 where m is unchanged, 0 before the first block.
+          const float f = m == m_new ? 1.f : ex2_approx(m - m_new);
+          if (i > 0) {
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * q, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(tO + 16 * q, o);
+            }
+          }
+          l *= f;
+          m = m_new;
+        }
+        {
+          uint32_t pk[kHalf / 2];
+          make_p(lo, ck, cm, bars->rv[tb], pk, l);
+          tmem_st32(tS, pk);  // P over keys 0..63 -> columns 0..31
+          tmem_wait_st();
+          tc_fence_before_sync();
+          mbar_arrive(&bars->p_full[t][0]);
+        }
+        if constexpr (D != 128) {
+          // d = 64 would spill with both halves live: its keys 64..127 are read again (P
+          // took columns 0..31 only, so their scores are intact)
+          uint32_t r[2][32];
+          tmem_ld32(tS + 64, r[0]);
+          tmem_ld32(tS + 96, r[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < kHalf; ++e) hi[e] = __uint_as_float(r[e >> 5][e & 31]);
+          if (shift > kHalf || lim < kBlockN) {
+#pragma unroll
+            for (int e = 0; e < kHalf; ++e)
+              if (e + kHalf < shift || e + kHalf >= lim) hi[e] = -INFINITY;
+          }
+        }
+        {
+          uint32_t pk[kHalf / 2];
+          make_p(hi, ck + 4, cm + 4, bars->rv[tb] + 4, pk, l);
+          tmem_st32(tS + 32, pk);  // keys 64..127 -> columns 32..63
+          tmem_wait_st();
+          tc_fence_before_sync();
+          mbar_arrive(&bars->p_full[t][1]);
+        }
+      }
+      // -------------------------------------------------------------- epilogue
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->o_full[t], 0, abort, wait_ns));
+      // Each warpgroup stages its normalised 128 x D tile in shared memory as D/32 panels
+      // of 128 rows x 128 B, swizzled like the tensor map (16-byte chunk q of row r at
+      // q ^ (r & 7): conflict-free for the per-row writes), and one thread stores the
+      // panels to o_part with TMA. Tile 0 finishes while tile 1's last PV may still read
+      // V from the slot ring, so it stages over the Q tiles (every QK has completed by
+      // o_full[0]); tile 1, last of all, stages over the ring. Rows past the unit's last
+      // row are stored too: they stay inside the chunk's 256-row slot, which no one reads.
+      const bool ok_all = bar_and(2 + t, 128, ok);
+      if (ok_all) {
+        tc_fence_after_sync();
+        constexpr int kOPanels = D / 32;  // 128-byte panels of an fp32 row
+        uint8_t* stage = smem + (t == 0 ? C::kQOff : C::kSlotOff);
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {  // panel q = columns [32 q, 32 q + 32)
+          uint32_t r[32];
+          tmem_ld32(tO + 32 * q, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(stage + q * (128 * 128) + row * 128 + ((e ^ (row & 7)) << 4)) =
+                make_float4(__uint_as_float(r[4 * e]) * inv, __uint_as_float(r[4 * e + 1]) * inv,
+                            __uint_as_float(r[4 * e + 2]) * inv, __uint_as_float(r[4 * e + 3]) * inv);
+        }
+        // this tile's partial: rows [128 t, 128 t + 128) of the chunk's slot
+        if (has_row) a.lse_part[(size_t)blockIdx.x * kUnitRows + t * 128 + row] = m - kOff + log2f(l);
+        fence_proxy_async_smem();  // the staged tile is read by the TMA unit
+        asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
+        if ((warp & 3) == 0 && lane == 0 && (alt || t * 128 < rows_here)) {
+#pragma unroll
+          for (int q = 0; q < kOPanels; ++q)
+            tma_store_2d(&P.tmap_o, stage + q * (128 * 128), 32 * q, (int)blockIdx.x * kUnitRows + t * 128);
+          bulk_commit();
+          bulk_wait_all();  // the shared memory must stay until the TMA has read it
+        }
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tbase, C::kTmemCols);
+  }
+  if (tid == 0) a.chunk_status[blockIdx.x] = (bars->abort ? kErrTimeout : 0u) | (bars->tree_err ? kErrBadTree : 0u);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (fn == nullptr) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
+// The codes of K or V viewed as [rows][H_kv][D] bytes; boxes of box_rows rows of one head.
+bool make_code_map(CUtensorMap* map, const void* base, int D, int Hkv, int64_t rows, int box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)Hkv * D};
+  cuuint32_t box[3] = {(cuuint32_t)D, 1, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Q viewed as [B*T nodes][H_kv][g][D] bf16; a box is 64 elements x g heads x one kv
+// head x tpu nodes, which lands as tpu*g consecutive 128-byte rows, node-major.
+bool make_q_map(CUtensorMap* map, const void* base, int D, const Plan& p) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.g, (cuuint64_t)p.Hkv, (cuuint64_t)(p.N > 0 ? p.N : 1)};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.g * D * 2, (cuuint64_t)p.Hq * D * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)p.g, 1, (cuuint32_t)p.tpu};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// o_part viewed as [n_chunks * 256 rows][D] fp32; boxes of 128 rows x 32 floats (128 B),
+// 128B-swizzled like the kernel's staging.
+bool make_o_map(CUtensorMap* map, float* base, int D, int64_t rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)(rows > 0 ? rows : 1)};
+  cuuint64_t strides[1] = {(cuuint64_t)D * 4};
+  cuuint32_t box[2] = {32, 128};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const Q8Args& a, cudaStream_t stream) {
+  TcParams P;
+  P.a = a;
+  const int box_rows = a.kv.page_size < kBlockN ? a.kv.page_size : kBlockN;
+  const int64_t rows = (int64_t)a.kv.num_pages * a.kv.page_size;
+  if (!make_q_map(&P.tmap_q, a.q, D, a.p) || !make_code_map(&P.tmap_k, a.kv.k_pages, D, a.p.Hkv, rows, box_rows) ||
+      !make_code_map(&P.tmap_v, a.kv.v_pages, D, a.p.Hkv, rows, box_rows) ||
+      !make_o_map(&P.tmap_o, a.o_part, D, (int64_t)a.p.n_chunks * kUnitRows))
+    return cudaErrorInvalidValue;
+  const int smem = smem_need<D>();
+  const cudaError_t e = cudaFuncSetAttribute(q8_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.p.n_chunks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.after_prep ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, q8_tc_kernel<D>, P);
+}
+
+}  // namespace
+
+cudaError_t launch_q8_tc(const Q8Args& a, cudaStream_t stream) {
+  if (a.p.n_chunks == 0) return cudaSuccess;
+  return a.p.d == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace ls

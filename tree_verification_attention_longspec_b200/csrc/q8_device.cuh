@@ -111,6 +111,7 @@ struct AppendArgs {
 };
 
 cudaError_t launch_q8_rows(const Q8Args& a, cudaStream_t stream);
+cudaError_t launch_q8_tc(const Q8Args& a, cudaStream_t stream);
 cudaError_t launch_q8_append(const AppendArgs& a, cudaStream_t stream);
 
 }  // namespace ls
