@@ -19,12 +19,13 @@
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warps 0-3, 4-7  softmax of tile 0, of tile 1
-//   warp 8          TMA producer: Q, then the blocks' codes (page by page) into a raw ring
+//   warp 8          TMA producer: Q, then the blocks' codes (page by page) into a raw ring;
+//                   the blocks' scales into a table
 //   warp 9          MMA issuer
 //   warps 10, 11    converters: raw tile -> swizzled f16 tile (cvt.f16x2.e4m3x2, two codes an
 //                   instruction; rows past the sequence become zeros, so that whatever they
-//                   hold meets weight 0 as 0), the block's scales into a table, and the
-//                   tree's keys and values from global memory
+//                   hold meets weight 0 as 0), and the tree's keys and values from
+//                   global memory
 // Converting in two warps costs the issue slots of ~700 instructions a warp and block, next
 // to the softmax's ~1000 a warp; reading 8-bit K and V by the tensor core itself would
 // need Q and P in 8 bits, P with them.
@@ -90,12 +91,14 @@ struct Bars {
   uint64_t s_full[kTiles];              // S_t(j) is in TMEM (and O_t holds every PV before it)
   uint64_t p_full[kTiles][2];           // half h of P_t(j) is in TMEM
   uint64_t o_full[kTiles];              // every MMA of tile t finished
+  uint64_t tree_full;                   // tree_max is there
   uint32_t tmem_base;
   uint32_t abort;
   uint32_t tree_err;                    // a parent link that is not a rooted tree's
   float kc[kTables][kGroups];           // key scales of the block's groups
   float lv[kTables][kGroups];           // log2 of the value scales
   float rv[kTables][kGroups];           // 1 / value scale
+  uint32_t tree_max[2];                 // largest magnitudes of the tree's keys and values (float bits)
   int8_t q_shift[kUnitRows];            // log2 of the row's power of two
   int16_t parent[kMaxTree];             // the sequence's tree (chunks that hold the tree block)
 };
@@ -136,6 +139,30 @@ __device__ __forceinline__ bool bar_and(uint32_t id, uint32_t n, bool pred) {
 __device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
   uint32_t never = 0;
   return mbar_wait_bounded(bar, parity, &never, kDrainNs);
+}
+
+// Largest magnitude of eight bf16 values, as the bits of one (ordered like the values), in
+// both halves of m; NaN is skipped.
+__device__ __forceinline__ void take_max(uint32_t (&m)[4], const uint4& w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) asm("max.bf16x2 %0, %0, %1;" : "+r"(m[e]) : "r"(u[e] & 0x7fff7fffu));
+}
+__device__ __forceinline__ float join_max(const uint32_t (&m)[4]) {
+  float x = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x = fmaxf(x, fmaxf(__uint_as_float(m[e] << 16), __uint_as_float(m[e] & 0xffff0000u)));
+  return x;
+}
+
+// Eight bf16 values times mul, as f16.
+__device__ __forceinline__ uint4 f16_of_bf16(const uint4& w, float mul) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    r[e] = pack_f16x2(__uint_as_float(u[e] << 16) * mul, __uint_as_float(u[e] & 0xffff0000u) * mul);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // P for 64 scores of four groups: 2^(s * ck + cm), packed to f16 pairs; adds each group's
@@ -272,6 +299,17 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     if (a.after_prep) asm volatile("griddepcontrol.wait;" ::: "memory");
   };
 
+  // Block j's scale table, lane g writing group g's entries (one whole warp).
+  auto write_scales = [&](int j, float k, float lv, float rv) {
+    if (lane < kGroups) {
+      bars->kc[j % kTables][lane] = k;
+      bars->lv[j % kTables][lane] = lv;
+      bars->rv[j % kTables][lane] = rv;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->table_full[j % kTables]);
+  };
+
   if (warp == kProducerWarp && lane == 0) {
     mbar_init(&bars->q_full, 1);
     for (int s = 0; s < C::kRaw; ++s) {
@@ -289,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
       mbar_init(&bars->p_full[t][1], 128);
       mbar_init(&bars->o_full[t], 1);
     }
+    mbar_init(&bars->tree_full, 8);
+    bars->tree_max[0] = bars->tree_max[1] = 0u;
     bars->abort = 0u;
     bars->tree_err = 0u;
     fence_mbar_init();
@@ -315,6 +355,16 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     const int n_pages = (seq_len + kv.page_size - 1) / kv.page_size;
     int issued = 0, slot = 0, use = 0;
     bool ok = true;
+    // A block's scales are read when its keys are asked for, and go into the table one block
+    // later, when they have come.
+    float ks = 1.f, vs = 1.f;
+    int scaled = -1;  // the block whose scales ks, vs hold
+    auto put_scales = [&]() {
+      if (scaled < 0) return;
+      const float v = fminf(fmaxf(vs, 8.6736174e-19f), 1.8446744e19f);
+      write_scales(scaled, fmaxf(ks, 1.17549435e-38f), log2f(v), 1.f / v);
+      scaled = -1;
+    };
     if (lane == 0 && !a.after_prep) {
       mbar_arrive_expect_tx(&bars->q_full, C::kPanels * 128 * p.g * p.tpu);
 #pragma unroll
@@ -348,6 +398,18 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         const int32_t page = kv.page_table[(size_t)c.b * kv.max_pages + lp];
         prow = ((uint32_t)page < (uint32_t)kv.num_pages ? page : 0) * kv.page_size + key % kv.page_size;
       }
+      if (!val) {
+        put_scales();
+        const int key = lane * kGroup;  // lane g: group g's row, from the lane that has its box
+        const int row = __shfl_sync(0xffffffffu, prow, min(key / bh, 31)) + key % bh;
+        ks = vs = 1.f;
+        if (lane < kGroups && c.key_begin + j * kBlockN + key < c.key_end) {
+          const size_t at = (size_t)(row / kv.scale_block) * p.Hkv + c.kh;
+          ks = __ldg(kv.k_scale + at);
+          vs = __ldg(kv.v_scale + at);
+        }
+        scaled = j;
+      }
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->raw_empty[slot], (use & 1) ^ 1, abort, wait_ns));
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[slot], C::kRawBytes);
@@ -361,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         ++use;
       }
     }
+    put_scales();
     if (!q_issued) {  // no prefix tile at all
       wait_prior();
       if (lane == 0) {
@@ -380,28 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
   } else if (warp >= kConvertWarp) {
     // ------------------------------------------------------------------ converters
     const int ct = tid - kConvertWarp * 32;  // 0 .. 63
-    // a block's scales: lane g of the first warp holds group g's, read one block ahead
-    float ks = 1.f, vs = 1.f;
-    auto read_scales = [&](int j) {
-      const int key = c.key_begin + j * kBlockN + lane * kGroup;
-      ks = vs = 1.f;
-      if (lane < kGroups && key < c.key_end) {
-        const size_t at = (size_t)(q8_row(kv, c.b, c.key_skip + key) / kv.scale_block) * p.Hkv + c.kh;
-        ks = __ldg(kv.k_scale + at);
-        vs = __ldg(kv.v_scale + at);
-      }
-    };
-    auto write_scales = [&](int j, float k, float lv, float rv) {
-      if (lane < kGroups) {
-        bars->kc[j % kTables][lane] = k;
-        bars->lv[j % kTables][lane] = lv;
-        bars->rv[j % kTables][lane] = rv;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->table_full[j % kTables]);
-    };
     const bool first_warp = warp == kConvertWarp;
-    if (first_warp) read_scales(0);
     int slot = 0, use = 0, raw = 0, raw_use = 0;
     bool ok = true;
     for (int ld = 0; ld < n_tiles && ok; ++ld) {
@@ -411,11 +453,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
       if (!ok) break;
       uint8_t* dst = smem + C::kSlotOff + slot * C::kTileBytes;
       if (j < nb) {
-        if (first_warp && !val) {  // its scales, before any score of it exists
-          const float v = fminf(fmaxf(vs, 8.6736174e-19f), 1.8446744e19f);
-          write_scales(j, fmaxf(ks, 1.17549435e-38f), log2f(v), 1.f / v);
-          if (j + 1 < nb) read_scales(j + 1);
-        }
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->raw_full[raw], raw_use & 1, abort, wait_ns));
         if (!ok) break;
         const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
@@ -458,45 +495,35 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
           ++raw_use;
         }
       } else {
-        // The tree block: bf16 rows from global memory, times a power of two for the tile.
-        // Each warp finds the tile's largest magnitude by itself (no barrier between two warps
-        // of which one may have given up).
+        // The tree block: bf16 rows from global memory, times a power of two for the tile (its
+        // largest magnitude has been found by the softmax warps).
         constexpr int kChunks = D / 8;  // 16-byte chunks of a bf16 row
-        const size_t stride = (size_t)p.Hkv * D, head = ((size_t)tree_base * p.Hkv + c.kh) * D;
-        if (!val) wait_prior();
-        auto largest = [&](const uint16_t* from) {
-          float amax = 0.f;
-          for (int i = lane; i < tree_n * kChunks; i += 32) {
-            const uint4 w = *reinterpret_cast<const uint4*>(from + (size_t)(i / kChunks) * stride + (i % kChunks) * 8);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        constexpr int kIter = 128 * kChunks / kConverters, kBatch = 8;
+        if (!val) {
+          wait_prior();
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->tree_full, 0, abort, wait_ns));
+          if (!ok) break;
+        }
+        const int vsh = min(max(f16_shift(__uint_as_float(bars->tree_max[1])), -kMaxScaleExp), -kMinScaleExp);
+        const int ksh = f16_shift(__uint_as_float(bars->tree_max[0]));
+        if (first_warp && !val) write_scales(j, pow2f(-ksh), (float)-vsh, pow2f(vsh));  // all groups alike
+        const float mul = pow2f(val ? vsh : ksh);
+        const uint16_t* from = (val ? a.v_tree : a.k_tree) + ((size_t)tree_base * p.Hkv + c.kh) * D;
+#pragma unroll 1
+        for (int it = 0; it < kIter; it += kBatch) {
+          uint4 w[kBatch];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+          for (int e = 0; e < kBatch; ++e) {
+            const int i = ct + (it + e) * kConverters, row = i / kChunks;
+            w[e] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < tree_n) w[e] = *reinterpret_cast<const uint4*>(from + (size_t)row * p.Hkv * D + i % kChunks * 8);
           }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          return amax;
-        };
-        auto value_shift = [&]() {
-          return min(max(f16_shift(largest(a.v_tree + head)), -kMaxScaleExp), -kMinScaleExp);
-        };
-        const uint16_t* from = (val ? a.v_tree : a.k_tree) + head;
-        const int sh = val ? value_shift() : f16_shift(largest(from));
-        if (first_warp && !val) {  // the block's table: all groups alike
-          const int vsh = value_shift();
-          write_scales(j, pow2f(-sh), (float)-vsh, pow2f(vsh));
-        }
-        const float mul = pow2f(sh);
-        for (int i = ct; i < 128 * kChunks; i += kConverters) {
-          const int row = i / kChunks, cc = i % kChunks;
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (row < tree_n) w = *reinterpret_cast<const uint4*>(from + (size_t)row * stride + cc * 8);
-          uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * mul, __uint_as_float(u[e] & 0xffff0000u) * mul);
-          *reinterpret_cast<uint4*>(dst + (cc / 8) * C::kPanelBytes + row * 128 + (((cc % 8) ^ (row & 7)) << 4)) =
-              make_uint4(u[0], u[1], u[2], u[3]);
+          for (int e = 0; e < kBatch; ++e) {
+            const int i = ct + (it + e) * kConverters, row = i / kChunks, cc = i % kChunks;
+            *reinterpret_cast<uint4*>(dst + (cc / 8) * C::kPanelBytes + row * 128 + (((cc % 8) ^ (row & 7)) << 4)) =
+                f16_of_bf16(w[e], mul);
+          }
         }
       }
       fence_proxy_async_smem();  // the tile is read by the tensor core
@@ -514,35 +541,49 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     // that starts at the lane, so that a warp's accesses spread over the banks. The rows
     // after the box's tpu * g become zeros, so that no stale shared memory enters an MMA.
     if (warp < 8) {
+      if (has_tree) {
+        // the largest magnitudes of the tree block's keys and values, while Q and the first
+        // keys are on their way
+        wait_prior();
+#pragma unroll
+        for (int val = 0; val < 2; ++val) {
+          constexpr int kChunks = D / 8;
+          const uint16_t* from = (val ? a.v_tree : a.k_tree) + ((size_t)tree_base * p.Hkv + c.kh) * D;
+          uint32_t m[4] = {0u, 0u, 0u, 0u};
+          uint4 w[kChunks / 2];  // 128 rows over 256 threads
+#pragma unroll
+          for (int e = 0; e < kChunks / 2; ++e) {
+            const int i = tid + 256 * e, row = i / kChunks;
+            w[e] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < tree_n) w[e] = *reinterpret_cast<const uint4*>(from + (size_t)row * p.Hkv * D + i % kChunks * 8);
+          }
+#pragma unroll
+          for (int e = 0; e < kChunks / 2; ++e) take_max(m, w[e]);
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(join_max(m)));
+          if (lane == 0) atomicMax(&bars->tree_max[val], most);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->tree_full);
+      }
       const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->q_full, 0, abort, wait_ns));
       if (got) {
         const bool row_there = tid < p.tpu * p.g;
         uint8_t* line = smem + C::kQOff + tid * 128;
-        float amax = 0.f;
-        if (row_there) {
-#pragma unroll 4
-          for (int i = 0; i < C::kPanels * 8; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4*>(line + (i / 8) * C::kQPanelBytes + (((i + lane) & 7) << 4));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint4 w[C::kPanels * 8];
+        uint32_t m[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
-          }
+        for (int i = 0; i < C::kPanels * 8; ++i) {
+          w[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (row_there)
+            w[i] = *reinterpret_cast<const uint4*>(line + (i / 8) * C::kQPanelBytes + (((i + lane) & 7) << 4));
+          take_max(m, w[i]);
         }
-        const int sh = f16_shift(amax);
+        const int sh = f16_shift(join_max(m));
         const float mul = pow2f(sh);
         bars->q_shift[tid] = (int8_t)sh;
-#pragma unroll 4
-        for (int i = 0; i < C::kPanels * 8; ++i) {
-          uint4* at = reinterpret_cast<uint4*>(line + (i / 8) * C::kQPanelBytes + (((i + lane) & 7) << 4));
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (row_there) w = *at;
-          uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            u[e] = pack_f16x2(__uint_as_float(u[e] << 16) * mul, __uint_as_float(u[e] & 0xffff0000u) * mul);
-          *at = make_uint4(u[0], u[1], u[2], u[3]);
-        }
+        for (int i = 0; i < C::kPanels * 8; ++i)
+          *reinterpret_cast<uint4*>(line + (i / 8) * C::kQPanelBytes + (((i + lane) & 7) << 4)) = f16_of_bf16(w[i], mul);
       }
       fence_proxy_async_smem();
       // the tree of the sequence, for the tree mask; a parent outside [-1, T) is stored
@@ -718,8 +759,16 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
       for (int i = 0; i < n_mine; ++i) {
         const int j = alt ? 2 * i + t : i;  // the block
         const int tb = j % kTables;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->table_full[tb], (j / kTables) & 1, abort, wait_ns) &&
-                                         mbar_wait_bounded(&bars->s_full[t], i & 1, abort, wait_ns));
+        // the block's scales first (they came long ago), then its scores
+        float ck[kGroups], cm[kGroups];
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->table_full[tb], (j / kTables) & 1, abort, wait_ns));
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          // not 0 (a row or a block of zeros), so that a masked score stays -inf
+          ck[g] = fmaxf(bars->kc[tb][g] * cs, 1.17549435e-38f);
+          cm[g] = bars->lv[tb][g];
+        }
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&bars->s_full[t], i & 1, abort, wait_ns));
         if (!ok) break;
         tc_fence_after_sync();
         int shift = 0;  // masked leading columns (this row)
@@ -727,23 +776,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         const int lim = j == nb - 1 ? tail_end : kBlockN;  // columns from here on are masked
         const bool tree_blk = j == nb;                      // keys = the sequence's tree nodes
         if (tree_blk && mask_tree_scores(bars->parent, tS, has_row ? node : -1)) bars->tree_err = 1u;
-        // All 128 scores for the row maximum, kept in registers for both halves of P (P
-        // goes to columns 0..63, whose scores are in registers by then; d = 64 reads keys
-        // 64..127 again below).
+        // All 128 scores for the row maximum; the first half stays in registers for its P.
         float lo[kHalf];
         float hi[kHalf];
-        float ck[kGroups], cm[kGroups];
         float mx = -INFINITY;
         {
           uint32_t r[4][32];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, r[q]);
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            // not 0 (a row or a block of zeros), so that a masked score stays -inf
-            ck[g] = fmaxf(bars->kc[tb][g] * cs, 1.17549435e-38f);
-            cm[g] = bars->lv[tb][g];
-          }
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < kHalf; ++e) {
@@ -805,9 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
           tc_fence_before_sync();
           mbar_arrive(&bars->p_full[t][0]);
         }
-        if constexpr (D != 128) {
-          // d = 64 would spill with both halves live: its keys 64..127 are read again (P
-          // took columns 0..31 only, so their scores are intact)
+        {
+          // keys 64..127 are read again (P took columns 0..31 only, so their scores are
+          // intact): with both halves live the block's code spilled, and ran 9% longer
           uint32_t r[2][32];
           tmem_ld32(tS + 64, r[0]);
           tmem_ld32(tS + 96, r[1]);
