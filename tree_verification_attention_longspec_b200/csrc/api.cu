@@ -130,7 +130,8 @@ int make_plan(const ls_verify_dims* d, Plan* p, bool with_tree = true, const ls_
     if (blocks[b] > max_blocks) max_blocks = blocks[b];
   }
   const long long units = (long long)q.Hkv * q.rg;
-  const long long slots = sms;  // one prefix CTA per SM
+  // prefix CTAs that run at once: one per SM, two of the 8-row kind
+  const long long slots = slot_rows == 8 ? 2LL * sms : sms;
   const long long overhead = 2;  // per-chunk cost in blocks (Q load, partial store)
   int32_t best_C = max_blocks > 0 ? max_blocks : 1;
   long long best_cost = -1, best_n = 0;
@@ -465,6 +466,13 @@ ls::KvQ8 kv_args(const ls_kv_q8* kv) {
   k.scale_block = kv->scale_block;
   k.max_pages = kv->max_pages_per_seq;
   k.num_pages = (int32_t)kv->num_pages;
+  auto log2_of = [](int32_t x) {
+    int32_t s = 0;
+    while ((1 << s) < x) ++s;
+    return (1 << s) == x ? s : -1;
+  };
+  k.page_shift = log2_of(kv->page_size);
+  k.scale_shift = log2_of(kv->scale_block);
   return k;
 }
 

@@ -10,10 +10,11 @@
 // lies in f16's range, p and the codes are f16 operands (the codes exactly) and the scales
 // cost one FMA a score. out = O / l, lse = m - kOff + log2 l.
 //
-// Decoding and small trees read each cached byte for few rows: HBM bounds them. So no
-// shared memory on the way: every warp streams its own keys from global memory into
-// registers, 16 at a step, two steps ahead (8 KB a warp in flight at d = 128), converts
-// them there and feeds mma.sync with the cache as the A operand: S^T = K Q^T with 16 keys
+// Decoding and small trees read each cached byte for few rows: HBM bounds them, and what
+// keeps HBM busy is bytes in flight. Every warp streams its own keys, 16 at a step, through
+// its own ring in shared memory (cp.async, five steps ahead: 20 KB a warp, 160 KB an SM at
+// d = 128; no barrier but the warp's own), converts them in registers and feeds mma.sync
+// with the cache as the A operand: S^T = K Q^T with 16 keys
 // by 8 rows, O^T += V^T P^T with 16 dimensions by 8 rows, so that 8 rows cost half of what
 // a 16-row A operand would. The order of d inside a K step and of V's rows is free, and is
 // chosen so that a lane's operands are contiguous bytes: 32 of each of its two keys, 16 of
@@ -36,7 +37,6 @@ constexpr int kStep = 16;                // keys a warp takes at a time
 constexpr int kStride = kWarps * kStep;  // keys between a warp's steps
 constexpr float kRaise = 6.0f;           // log2 units that a score may exceed the running maximum by
 constexpr float kOff = 9.0f;             // so weights stay below 2^15
-static_assert(kStride == kBlockN, "a block is one step of every warp");
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -45,26 +45,39 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Of two packed bf16 values: the larger magnitude, and both times mul as f16.
+__device__ __forceinline__ float largest(uint32_t w) {
+  return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u)));
+}
+__device__ __forceinline__ uint32_t f16_of(uint32_t w, float mul) {
+  return pack_f16x2(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xffff0000u) * mul);
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ uint2 load8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void copy4(uint32_t to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
 
-// 16 cached keys and values as one lane holds them: with n = lane / 4, c = lane % 4, key
+// 16 cached keys and values as one lane multiplies them: with n = lane / 4, c = lane % 4, key
 // words of keys n and n + 8 (d = 16 c + 64 h .. + 15), value words of keys 2c, 2c + 1,
 // 2c + 8, 2c + 9 (d = n * D / 8 .. + D / 8 - 1).
 template <int D>
@@ -74,20 +87,38 @@ struct Frag {
   float ks, vs;
 };
 
-template <int D>
-constexpr int smem_bytes(int rows) {
-  return kWarps * rows * (D + 4) * 4;  // the warps' O (rows padded by 16 bytes)
-}
+// A warp's ring: kStages steps of 16 keys, 16 values and their scales. Chunk ch (16 bytes) of
+// key k's row sits at ch ^ f(k), which makes the fragments' reads free of bank conflicts at
+// d = 128 (at d = 64 two rows share a line, and the values' reads meet two to a bank).
+template <int D, int NT>
+struct Ring {
+  static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 6) : (NT == 1 ? 5 : 10);
+  static constexpr int kTile = kStep * D;         // bytes of a step's keys (or values)
+  static constexpr int kStage = 2 * kTile + 16;   // and the two scales
+  static constexpr int kBytes = kStages * kStage;  // a warp's
+  static __device__ __forceinline__ int place(int key, int ch) {
+    const int f = D == 128 ? (key & 7) ^ ((key & 1) << 2) : (key >> 1) & 3;
+    return key * D + ((ch ^ f) << 4);
+  }
+};
+
+// Two CTAs an SM where their registers allow it (units of 8 rows): more warps to hide a
+// step's chain of dependent instructions, and one CTA streams while the other starts or ends.
+constexpr int ctas_of(int nt) { return nt == 1 ? 2 : 1; }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const __grid_constant__ Q8Args a) {
+__global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __grid_constant__ Q8Args a) {
   constexpr int R = 8 * NT;          // rows of a unit
   constexpr int kKS = D / 16;        // K steps of a score
   constexpr int kMT = D / 16;        // 16-row tiles of O^T
   constexpr int kVB = D / 8;         // value bytes of a lane
   constexpr int kPad = D + 4;
-  extern __shared__ __align__(16) float so[];  // [warp][R][kPad]
-  __shared__ float sm[kWarps][R], sl[kWarps][R];
+  using Rg = Ring<D, NT>;
+  static_assert(ctas_of(NT) * (kWarps * Rg::kBytes + 3072) <= 228 * 1024, "shared memory");
+  static_assert(2 * R * kPad * 4 <= Rg::kBytes, "a warp's O, and its tree part's, take its ring's place");
+  static_assert(kWarps * kStep >= kMaxTree, "a step of every warp covers the tree");
+  extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings
+  __shared__ float sm[2][kWarps][R], sl[2][kWarps][R];
   __shared__ uint32_t vis[R][4];  // tree nodes visible to the row
   __shared__ int cut[R];          // window: first attended key the row sees
   __shared__ int16_t par[kMaxTree];
@@ -110,51 +141,48 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const __grid_const
   const KvQ8& kv = a.kv;
   const int64_t stride = (int64_t)p.Hkv * D;  // bytes of a cache row, elements of a tree row
 
-  // ---- the cache, two steps ahead
-  const uint8_t* kbase = kv.k_pages + c.kh * D + 16 * c4;
-  const uint8_t* vbase = kv.v_pages + c.kh * D + kVB * n;
+  // ---- the cache, kStages - 1 steps ahead
+  uint8_t* ring = smem + warp * Rg::kBytes;
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  constexpr int kChunks = D / 16, kCopies = kStep * kChunks / 32;  // 16-byte chunks of a row; a lane's of a tile
+  const int ch = lane % kChunks, kr = lane / kChunks;              // this lane's chunk, and row of the first copy
+  const uint8_t* kbase = kv.k_pages + c.kh * D + 16 * ch + kr * stride;
+  const uint8_t* vbase = kv.v_pages + c.kh * D + 16 * ch + kr * stride;
+  const float* sbase = (lane ? kv.v_scale : kv.k_scale) + c.kh;
   // cache row of the step's first key (a step never crosses a page: both are multiples of 16)
   auto find = [&](int key) -> int32_t { return key < c.key_end ? q8_row(kv, c.b, c.key_skip + key) : 0; };
-  auto load = [&](Frag<D>& f, int key, int32_t row) {
-    if (key >= c.key_end) return;
-    const uint8_t* k0 = kbase + (int64_t)(row + n) * stride;
+  auto copy = [&](int stage, int key, int32_t row) {
+    if (key < c.key_end) {
+      const uint32_t to = ring_at + stage * Rg::kStage;
+      const int64_t from = (int64_t)row * stride;
+      const uint8_t *kp = kbase + from, *vp = vbase + from;
 #pragma unroll
-    for (int hf = 0; hf < D / 64; ++hf) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint4 x = load16(k0 + 8 * j * stride + 64 * hf);
-        f.k[j][4 * hf] = x.x;
-        f.k[j][4 * hf + 1] = x.y;
-        f.k[j][4 * hf + 2] = x.z;
-        f.k[j][4 * hf + 3] = x.w;
+      for (int i = 0; i < kCopies; ++i) {
+        const int at = Rg::place(kr + i * (32 / kChunks), ch);
+        copy16(to + at, kp);
+        copy16(to + Rg::kTile + at, vp);
+        kp += stride * (32 / kChunks);
+        vp += stride * (32 / kChunks);
       }
+      if (lane < 2) copy4(to + 2 * Rg::kTile + 4 * lane, sbase + (int64_t)(row >> kv.scale_shift) * p.Hkv);
     }
-    const uint8_t* v0 = vbase + (int64_t)(row + 2 * c4) * stride;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint8_t* vp = v0 + ((j & 1) + 8 * (j >> 1)) * stride;
-      if constexpr (D == 128) {
-        const uint4 x = load16(vp);
-        f.v[j][0] = x.x;
-        f.v[j][1] = x.y;
-        f.v[j][2] = x.z;
-        f.v[j][3] = x.w;
-      } else {
-        const uint2 x = load8(vp);
-        f.v[j][0] = x.x;
-        f.v[j][1] = x.y;
-      }
-    }
-    const size_t s = (size_t)(row / kv.scale_block) * p.Hkv + c.kh;
-    f.ks = __ldg(kv.k_scale + s);
-    f.vs = __ldg(kv.v_scale + s);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  int key = c.key_begin + warp * kStep;
-  Frag<D> f0, f1;
-  int32_t r0 = find(key), r1 = find(key + kStride);
-  load(f0, key, r0);
-  load(f1, key + kStride, r1);
-  r0 = find(key + 2 * kStride);
+  // Lane l holds the row of this warp's step 32 * batch + l: one table read for 32 steps, and
+  // the next batch's is under way (a read a step held every copy up by its latency).
+  const int key0 = c.key_begin + warp * kStep;
+  auto find_batch = [&](int batch) { return find(key0 + (32 * batch + lane) * kStride); };
+  int32_t rows_now = find_batch(0), rows_next = find_batch(1);
+  int ahead = 0;  // the next step to copy
+  auto copy_next = [&](int stage) {
+    copy(stage, key0 + ahead * kStride, __shfl_sync(0xffffffffu, rows_now, ahead & 31));
+    if ((++ahead & 31) == 0) {
+      rows_now = rows_next;
+      rows_next = find_batch((ahead >> 5) + 1);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < Rg::kStages - 1; ++s) copy_next(s);
 
   // ---- per-row masks
   const bool win = p.window > 0 && c.key_begin < 2 * kBlockN && c.key_end > c.key_begin;
@@ -204,8 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const __grid_const
 #pragma unroll
       for (int s = 0; s < kKS; ++s) {
         w[s] = *reinterpret_cast<const uint2*>(qp + 64 * (s / 4) + 4 * (s % 4));
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(w[s].x << 16)), fabsf(__uint_as_float(w[s].x & 0xffff0000u))),
-                                 fmaxf(fabsf(__uint_as_float(w[s].y << 16)), fabsf(__uint_as_float(w[s].y & 0xffff0000u)))));
+        amax = fmaxf(amax, fmaxf(largest(w[s].x), largest(w[s].y)));
       }
     } else {
 #pragma unroll
@@ -217,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const __grid_const
     const float mul = pow2f(sh), inv = pow2f(-sh);
 #pragma unroll
     for (int s = 0; s < kKS; ++s) {
-      q[t][s][0] = pack_f16x2(__uint_as_float(w[s].x << 16) * mul, __uint_as_float(w[s].x & 0xffff0000u) * mul);
-      q[t][s][1] = pack_f16x2(__uint_as_float(w[s].y << 16) * mul, __uint_as_float(w[s].y & 0xffff0000u) * mul);
+      q[t][s][0] = f16_of(w[s].x, mul);
+      q[t][s][1] = f16_of(w[s].y, mul);
     }
     cs[t][0] = p.scale_log2 * __shfl_sync(0xffffffffu, inv, 8 * c4);
     cs[t][1] = p.scale_log2 * __shfl_sync(0xffffffffu, inv, 8 * c4 + 4);
@@ -287,29 +314,42 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const __grid_const
   };
 
   // ---- prefix steps
-  auto compute = [&](Frag<D>& f, int k0) {
-    float s[NT][4];
+  auto compute = [&](const uint8_t* tile, int k0) {
+    Frag<D> f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf) {
+        const uint4 x = *reinterpret_cast<const uint4*>(tile + Rg::place(n + 8 * j, c4 + 4 * hf));
+        f.k[j][4 * hf] = x.x;
+        f.k[j][4 * hf + 1] = x.y;
+        f.k[j][4 * hf + 2] = x.z;
+        f.k[j][4 * hf + 3] = x.w;
+      }
+    f.ks = reinterpret_cast<const float*>(tile + 2 * Rg::kTile)[0];
+    f.vs = reinterpret_cast<const float*>(tile + 2 * Rg::kTile)[1];
+    float s[NT][4], s2[NT][4];  // two chains of products
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[t][e] = s2[t][e] = 0.f;
 #pragma unroll
     for (int i = 0; i < kKS; ++i) {
       const uint32_t a0 = e4m3x2_f16x2(f.k[0][i]), a1 = e4m3x2_f16x2(f.k[1][i]);
       const uint32_t a2 = e4m3x2_f16x2_hi(f.k[0][i]), a3 = e4m3x2_f16x2_hi(f.k[1][i]);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) mma16816(s[t], a0, a1, a2, a3, q[t][i][0], q[t][i][1]);
+      for (int t = 0; t < NT; ++t) mma16816(i & 1 ? s2[t] : s[t], a0, a1, a2, a3, q[t][i][0], q[t][i][1]);
     }
     // scales: a key's below f32's normals counts as 2^-126 (its scores are 0 either way), a
     // value's as the nearer end of [2^-60, 2^64]
     const float ks = fmaxf(f.ks, 1.17549435e-38f);
     const float vs = fminf(fmaxf(f.vs, 8.6736174e-19f), 1.8446744e19f);
-    const float lv = log2f(vs), rv = 1.f / vs;
+    const float lv = lg2_approx(vs), rv = rcp_approx(vs);  // off by 2^-22, like the exponentials
     const bool edge = k0 + kStep > c.key_end;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = fmaf(s[t][e], ks * cs[t][e & 1], lv);
+      for (int e = 0; e < 4; ++e) s[t][e] = fmaf(s[t][e] + s2[t][e], ks * cs[t][e & 1], lv);
     if (edge || win) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -318,6 +358,23 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const __grid_const
           const int kk = k0 + n + 8 * (e >> 1);
           if (kk >= c.key_end || kk < cuts[t][e & 1]) s[t][e] = -INFINITY;
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int kk = 2 * c4 + (j & 1) + 8 * (j >> 1);
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(tile + Rg::kTile + Rg::place(kk, n));
+        f.v[j][0] = x.x;
+        f.v[j][1] = x.y;
+        f.v[j][2] = x.z;
+        f.v[j][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(tile + Rg::kTile + Rg::place(kk, n >> 1) + 8 * (n & 1));
+        f.v[j][0] = x.x;
+        f.v[j][1] = x.y;
+      }
+    }
+    {
       if (edge) {  // rows past the sequence hold anything: no NaN into the product
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -341,136 +398,141 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const __grid_const
       }
     }
   };
-  while (key < c.key_end) {
-    compute(f0, key);
-    r1 = find(key + 3 * kStride);
-    load(f0, key + 2 * kStride, r0);
-    if (key + kStride < c.key_end) compute(f1, key + kStride);
-    r0 = find(key + 4 * kStride);
-    load(f1, key + 3 * kStride, r1);
-    key += 2 * kStride;
+  int stage = 0;
+  for (int key = key0; key < c.key_end; key += kStride) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(Rg::kStages - 2) : "memory");
+    __syncwarp();  // the stage is there for every lane, and every lane is done with the one before
+    copy_next(stage == 0 ? Rg::kStages - 1 : stage - 1);
+    compute(ring + stage * Rg::kStage, key);
+    stage = stage == Rg::kStages - 1 ? 0 : stage + 1;
   }
-
-  // ---- the tree block: bf16 keys and values, 16 a step, scaled into f16 by powers of two
-  // (a key's own, and one for the step's values, which then act as a value scale)
-  if (c.has_tree) {
-    for (int x0 = warp * kStep; x0 < tree_n; x0 += kStride) {
-      float s[NT][4];
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+  // This warp's result into its ring's place: its rows' maxima and sums, and O^T. (The tree
+  // block starts anew: carried along, its registers spilled into the loop above.)
+  auto put = [&](int part) {
+    float* to = reinterpret_cast<float*>(ring) + part * R * kPad;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-      uint32_t kh[2][kKS][2];
-      float kinv[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int x = x0 + n + 8 * j;
-        uint2 w[kKS];
-        float amax = 0.f;
-        const uint16_t* kp = a.k_tree + (int64_t)(tree_base + x) * stride + c.kh * D + 16 * c4;
-#pragma unroll
-        for (int i = 0; i < kKS; ++i) {
-          w[i] = x < tree_n ? *reinterpret_cast<const uint2*>(kp + 64 * (i / 4) + 4 * (i % 4)) : make_uint2(0u, 0u);
-          amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(w[i].x << 16)), fabsf(__uint_as_float(w[i].x & 0xffff0000u))),
-                                   fmaxf(fabsf(__uint_as_float(w[i].y << 16)), fabsf(__uint_as_float(w[i].y & 0xffff0000u)))));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int sh = f16_shift(amax);
-        const float mul = pow2f(sh);
-        kinv[j] = pow2f(-sh);
-#pragma unroll
-        for (int i = 0; i < kKS; ++i) {
-          kh[j][i][0] = pack_f16x2(__uint_as_float(w[i].x << 16) * mul, __uint_as_float(w[i].x & 0xffff0000u) * mul);
-          kh[j][i][1] = pack_f16x2(__uint_as_float(w[i].y << 16) * mul, __uint_as_float(w[i].y & 0xffff0000u) * mul);
+      for (int e = 0; e < 2; ++e) {
+        float s = l[t][e];
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+        s += __shfl_xor_sync(0xffffffffu, s, 16);
+        if (n == 0) {
+          sm[part][warp][8 * t + 2 * c4 + e] = m[t][e];
+          sl[part][warp][8 * t + 2 * c4 + e] = s;
         }
       }
 #pragma unroll
-      for (int i = 0; i < kKS; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(s[t], kh[0][i][0], kh[1][i][0], kh[0][i][1], kh[1][i][1], q[t][i][0], q[t][i][1]);
-      // values: D / 8 of each of four nodes
-      uint32_t vw[4][kVB / 2];
-      float vmax = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int x = x0 + 2 * c4 + (j & 1) + 8 * (j >> 1);
-        const uint16_t* vp = a.v_tree + (int64_t)(tree_base + x) * stride + c.kh * D + kVB * n;
-#pragma unroll
-        for (int i = 0; i < kVB / 8; ++i) {
-          const uint4 w = x < tree_n ? *reinterpret_cast<const uint4*>(vp + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-          vw[j][4 * i] = w.x;
-          vw[j][4 * i + 1] = w.y;
-          vw[j][4 * i + 2] = w.z;
-          vw[j][4 * i + 3] = w.w;
-        }
-#pragma unroll
-        for (int i = 0; i < kVB / 2; ++i)
-          vmax = fmaxf(vmax, fmaxf(fabsf(__uint_as_float(vw[j][i] << 16)), fabsf(__uint_as_float(vw[j][i] & 0xffff0000u))));
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-      // all-zero values (or ones too small to matter in the sums) leave the weights as they are
-      const int vsh = min(max(f16_shift(vmax), -kMaxScaleExp), -kMinScaleExp);
-      const float vmul = pow2f(vsh), lv = (float)-vsh;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int x = x0 + n + 8 * (e >> 1);
-          const uint32_t* mask = vis[8 * t + 2 * c4 + (e & 1)];
-          const bool see = x < tree_n && ((mask[x >> 5] >> (x & 31)) & 1u);
-          s[t][e] = see ? fmaf(s[t][e] * kinv[e >> 1], cs[t][e & 1], lv) : -INFINITY;
-        }
-      uint32_t b[NT][2];
-      weigh(s, vmul, b);
-#pragma unroll
-      for (int i = 0; i < kMT; ++i) {  // values 2i (low half of word i) and 2i + 1
-        const uint32_t a0 = pack_f16x2(__uint_as_float(vw[0][i] << 16) * vmul, __uint_as_float(vw[1][i] << 16) * vmul);
-        const uint32_t a1 = pack_f16x2(__uint_as_float(vw[0][i] & 0xffff0000u) * vmul, __uint_as_float(vw[1][i] & 0xffff0000u) * vmul);
-        const uint32_t a2 = pack_f16x2(__uint_as_float(vw[2][i] << 16) * vmul, __uint_as_float(vw[3][i] << 16) * vmul);
-        const uint32_t a3 = pack_f16x2(__uint_as_float(vw[2][i] & 0xffff0000u) * vmul, __uint_as_float(vw[3][i] & 0xffff0000u) * vmul);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(o[t][i], a0, a1, a2, a3, b[t][0], b[t][1]);
+      for (int i = 0; i < kMT; ++i) {
+        float* at = to + (8 * t + 2 * c4) * kPad + kVB * n + 2 * i;
+        *reinterpret_cast<float2*>(at) = make_float2(o[t][i][0], o[t][i][2]);
+        *reinterpret_cast<float2*>(at + kPad) = make_float2(o[t][i][1], o[t][i][3]);
       }
     }
+  };
+  put(0);
+
+  // ---- the tree block: bf16 keys and values, 16 a step, scaled into f16 by powers of two
+  // (a key's own, and one for the step's values, which then act as a value scale). Both are
+  // read twice, for the power and for the product, rather than held.
+  const bool tree_here = c.has_tree && warp * kStep < tree_n;
+  if (tree_here) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
+    const int x0 = warp * kStep;
+    float s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+    auto key_word = [&](int j, int i) {
+      const int x = x0 + n + 8 * j;
+      const uint16_t* kp = a.k_tree + (int64_t)(tree_base + x) * stride + c.kh * D + 16 * c4;
+      return x < tree_n ? *reinterpret_cast<const uint2*>(kp + 64 * (i / 4) + 4 * (i % 4)) : make_uint2(0u, 0u);
+    };
+    float kmul[2], kinv[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < kKS; ++i) amax = fmaxf(amax, fmaxf(largest(key_word(j, i).x), largest(key_word(j, i).y)));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      kmul[j] = pow2f(f16_shift(amax));
+      kinv[j] = pow2f(-f16_shift(amax));
+    }
+#pragma unroll
+    for (int i = 0; i < kKS; ++i) {
+      const uint2 w0 = key_word(0, i), w1 = key_word(1, i);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mma16816(s[t], f16_of(w0.x, kmul[0]), f16_of(w1.x, kmul[1]), f16_of(w0.y, kmul[0]), f16_of(w1.y, kmul[1]),
+                 q[t][i][0], q[t][i][1]);
+    }
+    auto value_word = [&](int j, int i) {  // values 2i and 2i + 1 of the lane's node j
+      const int x = x0 + 2 * c4 + (j & 1) + 8 * (j >> 1);
+      const uint16_t* vp = a.v_tree + (int64_t)(tree_base + x) * stride + c.kh * D + kVB * n;
+      return x < tree_n ? *reinterpret_cast<const uint32_t*>(vp + 2 * i) : 0u;
+    };
+    float vmax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < kVB / 2; ++i) vmax = fmaxf(vmax, largest(value_word(j, i)));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+    // all-zero values (or ones too small to matter in the sums) leave the weights as they are
+    const int vsh = min(max(f16_shift(vmax), -kMaxScaleExp), -kMinScaleExp);
+    const float vmul = pow2f(vsh), lv = (float)-vsh;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int x = x0 + n + 8 * (e >> 1);
+        const uint32_t* mask = vis[8 * t + 2 * c4 + (e & 1)];
+        const bool see = x < tree_n && ((mask[x >> 5] >> (x & 31)) & 1u);
+        s[t][e] = see ? fmaf(s[t][e] * kinv[e >> 1], cs[t][e & 1], lv) : -INFINITY;
+      }
+    uint32_t b[NT][2];
+    weigh(s, vmul, b);
+#pragma unroll
+    for (int i = 0; i < kMT; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = f16_of(value_word(j, i), vmul);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mma16816(o[t][i], __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                 __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632), b[t][0], b[t][1]);
+    }
+    put(1);
   }
 
   // ---- the warps' results joined: rows' maxima and sums, then O^T weighted
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float s = l[t][e];
-      s += __shfl_xor_sync(0xffffffffu, s, 4);
-      s += __shfl_xor_sync(0xffffffffu, s, 8);
-      s += __shfl_xor_sync(0xffffffffu, s, 16);
-      if (n == 0) {
-        sm[warp][8 * t + 2 * c4 + e] = m[t][e];
-        sl[warp][8 * t + 2 * c4 + e] = s;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kMT; ++i) {
-      float* at = so + (size_t)(warp * R + 8 * t + 2 * c4) * kPad + kVB * n + 2 * i;
-      *reinterpret_cast<float2*>(at) = make_float2(o[t][i][0], o[t][i][2]);
-      *reinterpret_cast<float2*>(at + kPad) = make_float2(o[t][i][1], o[t][i][3]);
-    }
-  }
   __syncthreads();
+  const int parts = kWarps + (c.has_tree ? (tree_n + kStep - 1) / kStep : 0);  // then the tree's
   const size_t slot = (size_t)blockIdx.x * p.slot_rows;
   for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
     const int r = idx / (D / 4), d = idx % (D / 4) * 4;
     float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w][r]);
+    for (int w = 0; w < parts; ++w) M = fmaxf(M, sm[w / kWarps][w % kWarps][r]);
     const float ref = M == -INFINITY ? 0.f : M;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2_approx(sm[w][r] - ref);  // 0 for a warp that saw no key
-      L = fmaf(sl[w][r], f, L);
-      const float4 v = *reinterpret_cast<const float4*>(so + (size_t)(w * R + r) * kPad + d);
+    for (int w = 0; w < parts; ++w) {
+      const float f = ex2_approx(sm[w / kWarps][w % kWarps][r] - ref);  // 0 for a warp that saw no key
+      L = fmaf(sl[w / kWarps][w % kWarps][r], f, L);
+      const float* from = reinterpret_cast<const float*>(smem + (w % kWarps) * Rg::kBytes) + (w / kWarps) * R * kPad;
+      const float4 v = *reinterpret_cast<const float4*>(from + r * kPad + d);
       acc.x = fmaf(v.x, f, acc.x);
       acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z);
@@ -485,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_rows_kernel(const __grid_const
 
 template <int D, int NT>
 cudaError_t launch(const Q8Args& a, cudaStream_t stream) {
-  const int smem = smem_bytes<D>(8 * NT);
-  if (smem > 48 * 1024) {
+  const int smem = kWarps * Ring<D, NT>::kBytes;
+  {
     const cudaError_t e = cudaFuncSetAttribute(q8_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }

@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         const int row = __shfl_sync(0xffffffffu, prow, min(key / bh, 31)) + key % bh;
         ks = vs = 1.f;
         if (lane < kGroups && c.key_begin + j * kBlockN + key < c.key_end) {
-          const size_t at = (size_t)(row / kv.scale_block) * p.Hkv + c.kh;
+          const size_t at = (size_t)(row >> kv.scale_shift) * p.Hkv + c.kh;
           ks = __ldg(kv.k_scale + at);
           vs = __ldg(kv.v_scale + at);
         }
@@ -457,35 +457,34 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         if (!ok) break;
         const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
         const int lim = j == nb - 1 ? tail_end : kBlockN;
-        constexpr int kChunks = D / 16;  // 16-byte chunks of a raw row
-        constexpr int kIter = 128 * kChunks / kConverters;
-        constexpr int kBatch = 8;
+        // A thread takes one 16-byte chunk column of every kRows-th row (kRows a multiple of 8,
+        // so that the swizzle stays its own: chunk q of a panel row sits at q ^ (row & 7)). At
+        // d = 128, eight lanes hold four chunks of two rows each: their stores then cover all
+        // bank groups, and only the (half as many) loads meet two to a bank.
+        constexpr int kChunks = D / 16, kRows = kConverters / kChunks, kIter = 128 / kRows, kBatch = 8;
+        const int cc = D == 128 ? (ct & 3) | ((ct >> 1) & 4) : ct & 3;
+        const int row0 = D == 128 ? ((ct >> 2) & 1) | ((ct >> 3) & 2) | ((ct >> 3) & 4) : ct >> 2;
+        uint8_t* line = dst + (cc / 4) * C::kPanelBytes + row0 * 128;
+        uint8_t* first = line + (((2 * (cc & 3)) ^ (row0 & 7)) << 4);
+        uint8_t* second = line + (((2 * (cc & 3) + 1) ^ (row0 & 7)) << 4);
+        src += row0 * D + cc * 16;
 #pragma unroll
         for (int it = 0; it < kIter; it += kBatch) {
           uint4 w[kBatch];
 #pragma unroll
-          for (int e = 0; e < kBatch; ++e) w[e] = *reinterpret_cast<const uint4*>(src + (ct + (it + e) * kConverters) * 16);
+          for (int e = 0; e < kBatch; ++e) w[e] = *reinterpret_cast<const uint4*>(src + (it + e) * kRows * D);
+          if (lim < kBlockN) {
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+              if (row0 + (it + e) * kRows >= lim) w[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
 #pragma unroll
           for (int e = 0; e < kBatch; ++e) {
-            const int i = ct + (it + e) * kConverters;
-            const int row = i / kChunks, cc = i % kChunks;
-            if (row >= lim) w[e] = make_uint4(0u, 0u, 0u, 0u);
-            uint4 x, y;
-            x.x = e4m3x2_f16x2(w[e].x);
-            x.y = e4m3x2_f16x2_hi(w[e].x);
-            x.z = e4m3x2_f16x2(w[e].y);
-            x.w = e4m3x2_f16x2_hi(w[e].y);
-            y.x = e4m3x2_f16x2(w[e].z);
-            y.y = e4m3x2_f16x2_hi(w[e].z);
-            y.z = e4m3x2_f16x2(w[e].w);
-            y.w = e4m3x2_f16x2_hi(w[e].w);
-            // chunk q of a panel row sits at q ^ (row & 7); the upper panel's lanes store their
-            // second half first, so that a row's eight lanes cover all eight bank groups
-            uint8_t* line = dst + (cc / 4) * C::kPanelBytes + row * 128;
-            const int q0 = 2 * (cc % 4), sw = row & 7;
-            const bool flip = cc >= 4;
-            *reinterpret_cast<uint4*>(line + (((q0 + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? y : x;
-            *reinterpret_cast<uint4*>(line + (((q0 + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? x : y;
+            const int at = (it + e) * kRows * 128;
+            *reinterpret_cast<uint4*>(first + at) =
+                make_uint4(e4m3x2_f16x2(w[e].x), e4m3x2_f16x2_hi(w[e].x), e4m3x2_f16x2(w[e].y), e4m3x2_f16x2_hi(w[e].y));
+            *reinterpret_cast<uint4*>(second + at) =
+                make_uint4(e4m3x2_f16x2(w[e].z), e4m3x2_f16x2_hi(w[e].z), e4m3x2_f16x2(w[e].w), e4m3x2_f16x2_hi(w[e].w));
           }
         }
         __syncwarp();

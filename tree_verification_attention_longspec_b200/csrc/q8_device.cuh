@@ -21,12 +21,13 @@ struct KvQ8 {
   float* v_scale;
   const int32_t* page_table;  // [B][max_pages]
   int32_t page_size, scale_block, max_pages, num_pages;
+  int32_t page_shift, scale_shift;  // their log2 (page_shift -1 where the page is no power of two)
 };
 
 // First row of the page that holds key `key` of sequence b, plus the key's place in it. A
 // table entry outside the cache reads page 0 instead (no fault, the result is unspecified).
 __device__ __forceinline__ int32_t q8_row(const KvQ8& kv, int32_t b, int32_t key) {
-  int32_t lp = key / kv.page_size;
+  int32_t lp = kv.page_shift >= 0 ? key >> kv.page_shift : key / kv.page_size;
   const int32_t in = key - lp * kv.page_size;
   if (lp >= kv.max_pages) lp = kv.max_pages - 1;
   const int32_t page = kv.page_table[(size_t)b * kv.max_pages + lp];
