@@ -31,10 +31,7 @@ namespace ls {
 namespace {
 using sm100::ex2_approx;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16;                // keys a warp takes at a time
-constexpr int kStride = kWarps * kStep;  // keys between a warp's steps
 constexpr float kRaise = 6.0f;           // log2 units that a score may exceed the running maximum by
 constexpr float kOff = 9.0f;             // so weights stay below 2^15
 
@@ -92,7 +89,7 @@ struct Frag {
 // d = 128 (at d = 64 two rows share a line, and the values' reads meet two to a bank).
 template <int D, int NT>
 struct Ring {
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 6) : (NT == 1 ? 5 : 10);
+  static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 4) : (NT == 1 ? 5 : 6);
   static constexpr int kTile = kStep * D;         // bytes of a step's keys (or values)
   static constexpr int kStage = 2 * kTile + 16;   // and the two scales
   static constexpr int kBytes = kStages * kStage;  // a warp's
@@ -102,23 +99,38 @@ struct Ring {
   }
 };
 
-// Two CTAs an SM where their registers allow it (units of 8 rows): more warps to hide a
-// step's chain of dependent instructions, and one CTA streams while the other starts or ends.
+// What a step costs is a chain of dependent instructions, so as many warps as their registers
+// allow: two CTAs of 8 an SM for units of 8 rows (one streams while the other starts or
+// ends), one of 12 for 16 rows.
+constexpr int warps_of(int nt) { return nt == 1 ? 8 : 12; }
 constexpr int ctas_of(int nt) { return nt == 1 ? 2 : 1; }
 
+// A tree of at most kQ8MaxRows rows has at most that many nodes: two steps.
+constexpr int kTreeSteps = 2;
+static_assert(kTreeSteps * kStep >= kQ8MaxRows, "tree steps");
+
+// The warps' rings, and the tree parts' O.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __grid_constant__ Q8Args a) {
+constexpr int smem_bytes() {
+  return warps_of(NT) * Ring<D, NT>::kBytes + kTreeSteps * 8 * NT * (D + 4) * 4;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * warps_of(NT), ctas_of(NT)) q8_rows_kernel(const __grid_constant__ Q8Args a) {
+  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps;
+  constexpr int kStride = kWarps * kStep;  // keys between a warp's steps
   constexpr int R = 8 * NT;          // rows of a unit
   constexpr int kKS = D / 16;        // K steps of a score
   constexpr int kMT = D / 16;        // 16-row tiles of O^T
   constexpr int kVB = D / 8;         // value bytes of a lane
   constexpr int kPad = D + 4;
   using Rg = Ring<D, NT>;
-  static_assert(ctas_of(NT) * (kWarps * Rg::kBytes + 3072) <= 228 * 1024, "shared memory");
-  static_assert(2 * R * kPad * 4 <= Rg::kBytes, "a warp's O, and its tree part's, take its ring's place");
-  static_assert(kWarps * kStep >= kMaxTree, "a step of every warp covers the tree");
+static_assert(ctas_of(NT) * (smem_bytes<D, NT>() + 8192) <= 228 * 1024, "shared memory");
+  static_assert(R * kPad * 4 <= Rg::kBytes, "a warp's O takes its ring's place");
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings
-  __shared__ float sm[2][kWarps][R], sl[2][kWarps][R];
+  __shared__ float sm[kWarps + kTreeSteps][R], sl[kWarps + kTreeSteps][R];  // the warps', then the tree's
+  __shared__ uint2 qs[NT][kKS][32];
+  __shared__ float q_inv[R];
   __shared__ uint32_t vis[R][4];  // tree nodes visible to the row
   __shared__ int cut[R];          // window: first attended key the row sees
   __shared__ int16_t par[kMaxTree];
@@ -217,13 +229,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
     for (int w = 0; w < 4; ++w) vis[tid][w] = m[w];
     cut[tid] = win ? window_cut(p, seq_len, depth) : 0;
   }
-  // ---- Q^T as B operands: row n of each row tile, f16, scaled by a power of two a row
+  // ---- Q^T as B operands, in shared memory (every warp multiplies by the same ones): row n of
+  // each row tile, f16, scaled by a power of two a row; warp t makes tile t's
   if (a.after_prep) asm volatile("griddepcontrol.wait;" ::: "memory");
-  uint32_t q[NT][kKS][2];
-  float cs[NT][2];  // score factor of rows 2c, 2c + 1: softmax scale * log2(e) / the row's power of two
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = 8 * t + n;
+  if (warp < NT) {
+    const int r = 8 * warp + n;
     uint2 w[kKS];
     float amax = 0.f;
     if (r < rows) {
@@ -241,21 +251,20 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const int sh = f16_shift(amax);
-    const float mul = pow2f(sh), inv = pow2f(-sh);
+    const float mul = pow2f(sh);
 #pragma unroll
-    for (int s = 0; s < kKS; ++s) {
-      q[t][s][0] = f16_of(w[s].x, mul);
-      q[t][s][1] = f16_of(w[s].y, mul);
-    }
-    cs[t][0] = p.scale_log2 * __shfl_sync(0xffffffffu, inv, 8 * c4);
-    cs[t][1] = p.scale_log2 * __shfl_sync(0xffffffffu, inv, 8 * c4 + 4);
+    for (int s = 0; s < kKS; ++s) qs[warp][s][lane] = make_uint2(f16_of(w[s].x, mul), f16_of(w[s].y, mul));
+    if (c4 == 0) q_inv[r] = pow2f(-sh);
   }
-  __syncthreads();  // vis, cut
+  __syncthreads();
+  float cs[NT][2];  // score factor of rows 2c, 2c + 1: softmax scale * log2(e) / the row's power of two
   int cuts[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     cuts[t][0] = cut[8 * t + 2 * c4];
     cuts[t][1] = cut[8 * t + 2 * c4 + 1];
+    cs[t][0] = p.scale_log2 * q_inv[8 * t + 2 * c4];
+    cs[t][1] = p.scale_log2 * q_inv[8 * t + 2 * c4 + 1];
   }
 
   float o[NT][kMT][4];
@@ -338,7 +347,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
       const uint32_t a0 = e4m3x2_f16x2(f.k[0][i]), a1 = e4m3x2_f16x2(f.k[1][i]);
       const uint32_t a2 = e4m3x2_f16x2_hi(f.k[0][i]), a3 = e4m3x2_f16x2_hi(f.k[1][i]);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) mma16816(i & 1 ? s2[t] : s[t], a0, a1, a2, a3, q[t][i][0], q[t][i][1]);
+      for (int t = 0; t < NT; ++t) {
+        const uint2 q = qs[t][i][lane];
+        mma16816(i & 1 ? s2[t] : s[t], a0, a1, a2, a3, q.x, q.y);
+      }
     }
     // scales: a key's below f32's normals counts as 2^-126 (its scores are 0 either way), a
     // value's as the nearer end of [2^-60, 2^64]
@@ -410,8 +422,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
   __syncwarp();
   // This warp's result into its ring's place: its rows' maxima and sums, and O^T. (The tree
   // block starts anew: carried along, its registers spilled into the loop above.)
+  auto part_of = [&](int part) {
+    return reinterpret_cast<float*>(smem + min(part, kWarps) * Rg::kBytes) + max(part - kWarps, 0) * R * kPad;
+  };
   auto put = [&](int part) {
-    float* to = reinterpret_cast<float*>(ring) + part * R * kPad;
+    float* to = part_of(part);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -421,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
         if (n == 0) {
-          sm[part][warp][8 * t + 2 * c4 + e] = m[t][e];
-          sl[part][warp][8 * t + 2 * c4 + e] = s;
+          sm[part][8 * t + 2 * c4 + e] = m[t][e];
+          sl[part][8 * t + 2 * c4 + e] = s;
         }
       }
 #pragma unroll
@@ -433,13 +448,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
       }
     }
   };
-  put(0);
+  put(warp);
 
-  // ---- the tree block: bf16 keys and values, 16 a step, scaled into f16 by powers of two
-  // (a key's own, and one for the step's values, which then act as a value scale). Both are
-  // read twice, for the power and for the product, rather than held.
-  const bool tree_here = c.has_tree && warp * kStep < tree_n;
-  if (tree_here) {
+  // ---- the tree block, a step for each of the last warps: bf16 keys and values, scaled into
+  // f16 by powers of two (a key's own, and one for the step's values, which then acts as their
+  // scale). Both are read twice, for the power and for the product, rather than held.
+  const int tree_step = kWarps - 1 - warp, x0 = tree_step * kStep;
+  if (c.has_tree && x0 < tree_n) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -449,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
       m[t][0] = m[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.f;
     }
-    const int x0 = warp * kStep;
     float s[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -475,9 +489,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
     for (int i = 0; i < kKS; ++i) {
       const uint2 w0 = key_word(0, i), w1 = key_word(1, i);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        mma16816(s[t], f16_of(w0.x, kmul[0]), f16_of(w1.x, kmul[1]), f16_of(w0.y, kmul[0]), f16_of(w1.y, kmul[1]),
-                 q[t][i][0], q[t][i][1]);
+      for (int t = 0; t < NT; ++t) {
+        const uint2 q = qs[t][i][lane];
+        mma16816(s[t], f16_of(w0.x, kmul[0]), f16_of(w1.x, kmul[1]), f16_of(w0.y, kmul[0]), f16_of(w1.y, kmul[1]), q.x,
+                 q.y);
+      }
     }
     auto value_word = [&](int j, int i) {  // values 2i and 2i + 1 of the lane's node j
       const int x = x0 + 2 * c4 + (j & 1) + 8 * (j >> 1);
@@ -515,24 +531,23 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
         mma16816(o[t][i], __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
                  __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632), b[t][0], b[t][1]);
     }
-    put(1);
+    put(kWarps + tree_step);
   }
 
   // ---- the warps' results joined: rows' maxima and sums, then O^T weighted
   __syncthreads();
-  const int parts = kWarps + (c.has_tree ? (tree_n + kStep - 1) / kStep : 0);  // then the tree's
+  const int parts = kWarps + (c.has_tree ? (tree_n + kStep - 1) / kStep : 0);
   const size_t slot = (size_t)blockIdx.x * p.slot_rows;
   for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
     const int r = idx / (D / 4), d = idx % (D / 4) * 4;
     float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < parts; ++w) M = fmaxf(M, sm[w / kWarps][w % kWarps][r]);
+    for (int w = 0; w < parts; ++w) M = fmaxf(M, sm[w][r]);
     const float ref = M == -INFINITY ? 0.f : M;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int w = 0; w < parts; ++w) {
-      const float f = ex2_approx(sm[w / kWarps][w % kWarps][r] - ref);  // 0 for a warp that saw no key
-      L = fmaf(sl[w / kWarps][w % kWarps][r], f, L);
-      const float* from = reinterpret_cast<const float*>(smem + (w % kWarps) * Rg::kBytes) + (w / kWarps) * R * kPad;
-      const float4 v = *reinterpret_cast<const float4*>(from + r * kPad + d);
+      const float f = ex2_approx(sm[w][r] - ref);  // 0 for a warp that saw no key
+      L = fmaf(sl[w][r], f, L);
+      const float4 v = *reinterpret_cast<const float4*>(part_of(w) + r * kPad + d);
       acc.x = fmaf(v.x, f, acc.x);
       acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z);
@@ -547,14 +562,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NT)) q8_rows_kernel(const __
 
 template <int D, int NT>
 cudaError_t launch(const Q8Args& a, cudaStream_t stream) {
-  const int smem = kWarps * Ring<D, NT>::kBytes;
-  {
-    const cudaError_t e = cudaFuncSetAttribute(q8_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  const int smem = smem_bytes<D, NT>();
+  static bool configured[kMaxConfigured] = {};  // per template instance
+  const cudaError_t e = configure_once(q8_rows_kernel<D, NT>, smem, configured);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.p.n_chunks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * warps_of(NT));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -985,7 +985,8 @@ cudaError_t launch(const Q8Args& a, cudaStream_t stream) {
       !make_o_map(&P.tmap_o, a.o_part, D, (int64_t)a.p.n_chunks * kUnitRows))
     return cudaErrorInvalidValue;
   const int smem = smem_need<D>();
-  const cudaError_t e = cudaFuncSetAttribute(q8_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static bool configured[kMaxConfigured] = {};  // per template instance
+  const cudaError_t e = configure_once(q8_tc_kernel<D>, smem, configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.p.n_chunks);

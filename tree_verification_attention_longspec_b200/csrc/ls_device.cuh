@@ -78,6 +78,20 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Opts a kernel in to `smem` bytes of dynamic shared memory, once per device (`configured`:
+// a static array of the caller's, one per kernel; two threads that race both set it).
+constexpr int kMaxConfigured = 64;
+template <class Kernel>
+cudaError_t configure_once(Kernel kernel, int smem, bool (&configured)[kMaxConfigured]) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < kMaxConfigured && configured[dev]) return cudaSuccess;
+  const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (f == cudaSuccess && dev >= 0 && dev < kMaxConfigured) configured[dev] = true;
+  return f;
+}
+
 }  // namespace ls
 
 // Launchers (defined in the kernel files, called by the host API).

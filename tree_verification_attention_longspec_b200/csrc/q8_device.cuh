@@ -14,6 +14,9 @@ namespace ls {
 // into its weight's exponent, and the sums take it out again, both in fp32.
 constexpr int kMinScaleExp = -60, kMaxScaleExp = 64;
 
+// Query rows of a kv head up to which the 8-bit cache streams through registers (attn_q8_rows.cu).
+constexpr int kQ8MaxRows = 32;
+
 struct KvQ8 {
   uint8_t* k_pages;  // [num_pages * page_size][Hkv][d]
   uint8_t* v_pages;

@@ -1172,8 +1172,8 @@ template <bool F32>
 int launch_sample(const SampleArgs& a, int64_t rows, int cluster, cudaStream_t st) {
   constexpr int smem = kDataBytes + (int)sizeof(Shared);
   static_assert(2 * (smem + 1024) <= 233472, "two CTAs an SM");
-  if (cudaFuncSetAttribute(sample_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return LS_ERR_CUDA;
+  static bool configured[kMaxConfigured] = {};  // per template instance
+  if (configure_once(sample_kernel<F32>, smem, configured) != cudaSuccess) return LS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * cluster));
   cfg.blockDim = dim3(kThreads);
