@@ -566,7 +566,9 @@ int run_append(ls::AppendArgs& a, const void* k_new, const void* v_new, const in
   a.rows = (int32_t)rows;
   // a sequence cannot append more than its table has room for
   a.max_new = (int32_t)std::min<int64_t>(max_new, (int64_t)kv->max_pages_per_seq * kv->page_size);
-  a.blocks = a.max_new > 0 ? (a.max_new - 1) / kv->scale_block + 2 : 0;
+  // n tokens touch at most (n - 1) / scale_block + 2 blocks, each sequence's and in all
+  const int64_t each = a.max_new > 0 ? (a.max_new - 1) / kv->scale_block + 2 : 0;
+  a.blocks = std::min<int64_t>(a.B * each, rows / kv->scale_block + 2ll * a.B);
   (void)cudaGetLastError();
   return ls::launch_q8_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LS_OK : LS_ERR_CUDA;
 }

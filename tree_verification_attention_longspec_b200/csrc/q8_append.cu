@@ -22,132 +22,169 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kKeep = 16;  // 16-byte loads a lane keeps between the passes
+constexpr int kBatch = 8;  // loads in flight past those
+
+// Rows that sequence b, of `len` tokens, appends.
+__device__ __forceinline__ int appended(const AppendArgs& a, int b, int len) {
+  int n = a.cu_new != nullptr ? a.cu_new[b + 1] - a.cu_new[b] : a.accept_len[b] + 1;
+  n = min(n, a.max_new);
+  const int64_t room = (int64_t)a.kv.max_pages * a.kv.page_size - len;
+  return n <= 0 || len < 0 ? 0 : (int)min((int64_t)n, max(room, (int64_t)0));
+}
+
+// The lengths after the call, by one CTA.
+__device__ void new_lengths(const AppendArgs& a) {
+  __shared__ int32_t part[kWarps * 32];
+  const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32);
+  const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int len = a.cu[b + 1] - a.cu[b];
+    sum += len + appended(a, b, len);
+  }
+  part[threadIdx.x] = sum;
+  __syncthreads();
+  int at = 0;
+  for (int t = 0; t < min((int)threadIdx.x, a.B); ++t) at += part[t];
+  if (threadIdx.x == 0) a.cu_out[0] = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int len = a.cu[b + 1] - a.cu[b];
+    at += len + appended(a, b, len);
+    a.cu_out[b + 1] = at;
+  }
+}
+
+// Eight bf16 values times (or, `divide`, over) s as codes.
+__device__ __forceinline__ uint2 encode(const uint4& v, float s, bool divide) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float x = __uint_as_float(w[k] << 16), y = __uint_as_float(w[k] & 0xffff0000u);
+    c[k] = divide ? f32x2_e4m3x2(__fdiv_rn(x, s), __fdiv_rn(y, s)) : f32x2_e4m3x2(x * s, y * s);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) q8_append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int kLanes = D / 8;         // lanes of a row
-  constexpr int kRows = 32 / kLanes;    // rows a step
-  const int lane = threadIdx.x & 31;
-  const KvQ8& kv = a.kv;
-  auto count = [&](int b, int len) -> int {  // rows that sequence b appends
-    int n;
-    if (a.cu_new != nullptr) {
-      n = a.cu_new[b + 1] - a.cu_new[b];
-    } else {
-      n = a.accept_len[b] + 1;
-    }
-    const int64_t room = (int64_t)kv.max_pages * kv.page_size - len;
-    n = min(n, a.max_new);
-    return n <= 0 || len < 0 ? 0 : (int)min((int64_t)n, max(room, (int64_t)0));
-  };
-  if (blockIdx.x == gridDim.x - 1) {  // the lengths after the call
-    if (a.cu_out == nullptr) return;
-    __shared__ int32_t part[kWarps * 32];
-    const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32);
-    const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      const int len = a.cu[b + 1] - a.cu[b];
-      sum += len + count(b, len);
-    }
-    part[threadIdx.x] = sum;
-    __syncthreads();
-    int at = 0;
-    for (int t = 0; t < (int)threadIdx.x; ++t) at += part[t];
-    if (threadIdx.x == 0) a.cu_out[0] = 0;
-    for (int b = b0; b < b1; ++b) {
-      const int len = a.cu[b + 1] - a.cu[b];
-      at += len + count(b, len);
-      a.cu_out[b + 1] = at;
-    }
+__global__ void __launch_bounds__(kWarps * 32, 2) q8_append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kLanes = D / 8;       // lanes of a row
+  constexpr int kRows = 32 / kLanes;  // rows a step
+  if (blockIdx.x == gridDim.x - 1) {
+    if (a.cu_out != nullptr) new_lengths(a);
     return;
   }
-  int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int h = (int)(id % a.Hkv);
-  id /= a.Hkv;
-  const bool val = id & 1;  // values, or keys
-  id >>= 1;
-  const int bl = (int)(id % a.blocks);
-  const int64_t b64 = id / a.blocks;
-  if (b64 >= a.B) return;
-  const int b = (int)b64;
-  const int len = a.cu[b + 1] - a.cu[b];
-  const int n = count(b, len);
-  const int block = len / kv.scale_block + bl;  // of the sequence
-  const int first = block * kv.scale_block;     // its first token
+  const int lane = threadIdx.x & 31;
+  const KvQ8& kv = a.kv;
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);  // (block, tensor, head)
+  const int h = (int)(unit % (uint32_t)a.Hkv);
+  const bool val = (unit / (uint32_t)a.Hkv) & 1;  // values, or keys
+  int id = (int)(unit / (uint32_t)a.Hkv >> 1);
+  // the touched blocks of all sequences in order: which one is number id?
+  int b = -1, len = 0, n = 0, block = 0;
+  for (int base = 0; base < a.B; base += 32) {
+    const int bb = base + lane;
+    const int l = bb < a.B ? a.cu[bb + 1] - a.cu[bb] : 0;
+    const int c = bb < a.B ? appended(a, bb, l) : 0;
+    const int touched = c > 0 ? ((l + c - 1) >> kv.scale_shift) - (l >> kv.scale_shift) + 1 : 0;
+    int upto = touched;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, id < upto);
+    if (here) {
+      const int at = __ffs(here) - 1;
+      b = base + at;
+      len = __shfl_sync(0xffffffffu, l, at);
+      n = __shfl_sync(0xffffffffu, c, at);
+      block = (len >> kv.scale_shift) + id - __shfl_sync(0xffffffffu, upto - touched, at);
+      break;
+    }
+    id -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (b < 0) return;
+  const int first = block * kv.scale_block;  // its first token
   const int p0 = max(len, first), p1 = min(len + n, first + kv.scale_block);
-  if (p0 >= p1) return;
-  const int page_no = first / kv.page_size;  // below max_pages: p0 is in the cache
-  const int32_t page = kv.page_table[(size_t)b * kv.max_pages + page_no];
-  if ((uint32_t)page >= (uint32_t)kv.num_pages) return;  // not a page of this cache: dropped
-  const int64_t row0 = (int64_t)page * kv.page_size + (first - page_no * kv.page_size);  // row of token `first`
   const int64_t stride = (int64_t)a.Hkv * D;
-  uint8_t* codes = (val ? kv.v_pages : kv.k_pages) + row0 * stride + h * D;
-  float* scale_at = (val ? kv.v_scale : kv.k_scale) + row0 / kv.scale_block * a.Hkv + h;
-  const uint16_t* src = (val ? a.v_new : a.k_new) + h * D;
-  // source row of the token at position p, -1 where the path names none
-  int tree_base = 0, tree_n = 0;
-  if (a.cu_new == nullptr) {
+  const int col = (lane % kLanes) * 8, sub = lane / kLanes;
+  const int steps = (p1 - p0 + kRows - 1) / kRows;
+
+  // The source row of token p0 + i: the next one, or where the path names it.
+  const int32_t* path = a.cu_new != nullptr ? nullptr : a.accept_path + (size_t)b * a.T + (p0 - len);
+  int row_base, row_end;  // rows of the sequence
+  if (path == nullptr) {
+    row_base = a.cu_new[b] + (p0 - len);
+    row_end = a.rows;
+  } else {
     Plan pl{};
     pl.B = a.B;
     pl.T = a.T;
     pl.N = a.rows;
-    tree_range(pl, a.cu_tree, b, &tree_base, &tree_n);
+    tree_range(pl, a.cu_tree, b, &row_base, &row_end);
+    row_end += row_base;
   }
-  auto source = [&](int p) -> int {
-    const int i = p - len;
-    if (a.cu_new != nullptr) {
-      const int r = a.cu_new[b] + i;
-      return (uint32_t)r < (uint32_t)a.rows ? r : -1;
-    }
-    const int node = a.accept_path[(size_t)b * a.T + i];
-    return (uint32_t)node < (uint32_t)tree_n ? tree_base + node : -1;
+  const uint16_t* src = (val ? a.v_new : a.k_new) + h * D + col;
+  auto source = [&](int i) -> int {  // -1: none
+    if (p0 + i >= p1) return -1;
+    const int r = path != nullptr ? path[i] : i;
+    return r >= 0 && row_base >= 0 && r < row_end - row_base ? row_base + r : -1;
   };
-  const int col = (lane % kLanes) * 8, sub = lane / kLanes;
-  const int steps = (p1 - p0 + kRows - 1) / kRows;
+  auto fetch = [&](int r) {
+    return r >= 0 ? *reinterpret_cast<const uint4*>(src + (int64_t)r * stride) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 keep[kKeep];
+  uint32_t there = 0u;  // bit s: row of step s exists
+#pragma unroll
+  for (int s = 0; s < kKeep; ++s) {
+    const int r = source(s * kRows + sub);
+    keep[s] = fetch(r);
+    there |= r >= 0 ? 1u << s : 0u;
+  }
+  // the block's place in the cache, while the rows are on their way
+  const int page_no = first / kv.page_size;  // below max_pages: p0 is in the cache
+  const int32_t page = kv.page_table[(size_t)b * kv.max_pages + page_no];
+  if ((uint32_t)page >= (uint32_t)kv.num_pages) return;  // not a page of this cache: dropped
+  const int64_t row0 = (int64_t)page * kv.page_size + (first - page_no * kv.page_size);  // row of token `first`
+  uint8_t* codes = (val ? kv.v_pages : kv.k_pages) + row0 * stride + h * D + col;
+  float* scale_at = (val ? kv.v_scale : kv.k_scale) + (row0 >> kv.scale_shift) * a.Hkv + h;
   const bool held = p0 > first;
   const float old = held ? *scale_at : 0.f;
 
-  uint4 keep[kKeep];
-  float amax = 0.f;
-  auto fetch = [&](int s, uint4& v) -> bool {
-    const int p = p0 + s * kRows + sub;
-    const int r = p < p1 ? source(p) : -1;
-    v = make_uint4(0u, 0u, 0u, 0u);
-    if (r >= 0) v = *reinterpret_cast<const uint4*>(src + (int64_t)r * stride + col);
-    return r >= 0;
+  // the largest magnitude: bf16 pairs compared as such (NaN skipped)
+  uint32_t most = 0u;
+  auto take = [&](const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm("max.bf16x2 %0, %0, %1;" : "+r"(most) : "r"(w[e] & 0x7fff7fffu));
   };
-  uint32_t there = 0u;  // bit s: row of step s exists
-  for (int s0 = 0; s0 < steps; s0 += kKeep) {
 #pragma unroll
-    for (int s = 0; s < kKeep; ++s) {
-      const bool ok = s0 + s < steps && fetch(s0 + s, keep[s]);
-      if (!ok) keep[s] = make_uint4(0u, 0u, 0u, 0u);
-      if (s0 == 0 && ok) there |= 1u << s;
-    }
+  for (int s = 0; s < kKeep; ++s) take(keep[s]);
+#pragma unroll 1
+  for (int s0 = kKeep; s0 < steps; s0 += kBatch) {
+    uint4 v[kBatch];
 #pragma unroll
-    for (int s = 0; s < kKeep; ++s) {
-      const uint32_t w[4] = {keep[s].x, keep[s].y, keep[s].z, keep[s].w};
+    for (int s = 0; s < kBatch; ++s) v[s] = fetch(source((s0 + s) * kRows + sub));
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-    }
+    for (int s = 0; s < kBatch; ++s) take(v[s]);
   }
+  float amax = fmaxf(__uint_as_float(most << 16), __uint_as_float(most & 0xffff0000u));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   // 448 = 1.75 * 2^8: amax = m * 2^k with 1 <= m < 2 needs e = k - 8, one more where m > 1.75
   int e = kMinScaleExp;
   if (amax > 0.f) {
-    const uint32_t bits = __float_as_uint(amax);
-    e = exponent_of(amax) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = exponent_of(amax) - 8 + ((__float_as_uint(amax) & 0x7fffffu) > 0x600000u ? 1 : 0);
     e = min(max(e, kMinScaleExp), kMaxScaleExp);
   }
   const float need = pow2f(e);
   const float now = held ? fmaxf(old, need) : need;
   if (held && old < now) {  // the earlier tokens' codes in the new unit
     const float ratio = old > 0.f ? old / now : 0.f;
+#pragma unroll 1
     for (int p = first + sub; p < p0; p += kRows) {
-      uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)(p - first) * stride + col);
+      uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)(p - first) * stride);
       uint2 c = *at;
       uint32_t* cw = reinterpret_cast<uint32_t*>(&c);
 #pragma unroll
@@ -162,34 +199,44 @@ __global__ void __launch_bounds__(kWarps * 32) q8_append_kernel(const __grid_con
     }
   }
   if (lane == 0 && !(held && old == now)) *scale_at = now;
-  auto store = [&](int s, const uint4& v) {
-    const int p = p0 + s * kRows + sub;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t c[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)  // a division: exact where the scale is a power of two
-      c[k] = f32x2_e4m3x2(__fdiv_rn(__uint_as_float(w[k] << 16), now),
-                          __fdiv_rn(__uint_as_float(w[k] & 0xffff0000u), now));
-    *reinterpret_cast<uint2*>(codes + (int64_t)(p - first) * stride + col) =
-        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  };
-  if (steps <= kKeep) {
+  codes += (int64_t)(p0 - first + sub) * stride;
+  auto store = [&](int s, const uint2& c) { *reinterpret_cast<uint2*>(codes + (int64_t)s * kRows * stride) = c; };
+  // a power of two (every scale of this kernel's) divides by a multiplication, exactly
+  if ((__float_as_uint(now) & 0x7fffffu) == 0u && now >= 1.17549435e-38f) {
+    const float inv = 1.f / now;
 #pragma unroll
     for (int s = 0; s < kKeep; ++s)
-      if (there >> s & 1u) store(s, keep[s]);
+      if (there >> s & 1u) store(s, encode(keep[s], inv, false));
+#pragma unroll 1
+    for (int s0 = kKeep; s0 < steps; s0 += kBatch) {
+      uint4 v[kBatch];
+      uint32_t have = 0u;
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const int r = source((s0 + s) * kRows + sub);
+        v[s] = fetch(r);
+        have |= r >= 0 ? 1u << s : 0u;
+      }
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s)
+        if (have >> s & 1u) store(s0 + s, encode(v[s], inv, false));
+    }
   } else {
+    // another writer's scale, kept: divisions, in a loop of their own (unrolled with the rest
+    // they were most of the kernel's code, and its time)
+#pragma unroll 1
     for (int s = 0; s < steps; ++s) {
-      uint4 v;
-      if (fetch(s, v)) store(s, v);
+      const int r = source(s * kRows + sub);
+      if (r >= 0) store(s, encode(fetch(r), now, true));
     }
   }
 }
 
 template <int D>
 cudaError_t launch_d(const AppendArgs& a, cudaStream_t stream) {
-  const int64_t warps = (int64_t)a.B * a.blocks * 2 * a.Hkv;
+  const int64_t warps = a.blocks * 2 * a.Hkv;
   const int64_t ctas = (warps + kWarps - 1) / kWarps + 1;  // the last one: the lengths
-  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  if (warps > INT32_MAX) return cudaErrorInvalidValue;
   q8_append_kernel<D><<<(unsigned)ctas, kWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }

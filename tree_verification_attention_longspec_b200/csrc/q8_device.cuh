@@ -111,7 +111,7 @@ struct AppendArgs {
   int32_t B, Hkv, d, T;
   int32_t rows;     // rows of k_new / v_new
   int32_t max_new;  // rows a sequence may append
-  int32_t blocks;   // scale blocks a sequence may touch
+  int64_t blocks;   // scale blocks that the sequences may touch in all
 };
 
 cudaError_t launch_q8_rows(const Q8Args& a, cudaStream_t stream);

@@ -48,19 +48,19 @@ def _refuse(t, name: str, dtypes, device, shape):
 def _ptr(t, name: str, dtype, device, shape=None):
     """The address of a dense CUDA tensor of this dtype, device and shape, or an error that
     names it. (One test on the way that every call takes: small calls are bound by it.)"""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or not t.is_contiguous()
-            or shape is not None and t.shape != shape):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device.index
+            or not t.is_contiguous() or shape is not None and t.shape != shape):
         _refuse(t, name, (dtype,), device, shape)
     return t.data_ptr()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _call(device, what: str, fn, *args):
     """fn(*args, stream) on `device` and its current stream; raises what it returns."""
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
