@@ -104,6 +104,7 @@ class KVCacheQ8:
                                     page_table.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                     k_scale.data_ptr(), v_scale.data_ptr())
         self._ref = ctypes.byref(self._struct)
+        self._kind = (self.batch, self.num_kv_heads, self.head_dim, self.device.index)
         # the writers' dims: batch, kv heads and head dimension (the tree size is the call's)
         self._dims = {}
 
@@ -200,26 +201,41 @@ class _AttnQ8:
             raise LSError(1, f"{self._name}_workspace_size returned 0 (invalid or unsupported dims)")
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
         self._ws_ptr = self.workspace.data_ptr()
+        self._fn = getattr(load_library(), self._name)
+        self._rows = batch * tree_size
+        self._kind = (batch, num_kv_heads, head_dim, dev.index)
+        self._shapes = self._shapes_of(self._rows)
 
-    def _check(self, q, cache, cu_seqlens, out, lse):
-        """(rows, q, cu_seqlens, out, lse addresses, out, lse)"""
-        d = self.dims
+    def _begin(self, q, cache, cu_seqlens, out, lse):
+        """(out, lse, the addresses of q, cu_seqlens, out, lse, and the shape of the tree's rows)"""
         if not isinstance(cache, KVCacheQ8):
             raise TypeError("cache must be a KVCacheQ8")
-        if (cache.batch, cache.num_kv_heads, cache.head_dim) != (d.batch, d.num_kv_heads, d.head_dim):
+        if cache._kind != self._kind:
+            if cache.device != self.device:
+                raise ValueError(f"the cache is on {cache.device}, the call on {self.device}")
             raise ValueError("the cache's batch, kv heads or head dimension are not the call's")
-        dev = self.device
-        if cache.device != dev:
-            raise ValueError(f"the cache is on {cache.device}, the call on {dev}")
-        rows = self.tree.total_nodes if self.tree is not None and self.tree.cu_tree else d.batch * d.tree_size
-        shape = (rows, d.num_q_heads, d.head_dim)
-        qp = _ptr(q, "q", torch.bfloat16, dev, shape)
+        dev, d = self.device, self.dims
+        rows = self.tree.total_nodes if self.tree is not None and self.tree.cu_tree else self._rows
+        if rows != self._shapes[3][0]:
+            self._shapes = self._shapes_of(rows)
+        q_shape, lse_shape, cu_shape, kv_shape = self._shapes
+        qp = _ptr(q, "q", torch.bfloat16, dev, q_shape)
         if out is None:
             out = torch.empty_like(q)
+            op = out.data_ptr()
+        else:
+            op = _ptr(out, "out", torch.bfloat16, dev, q_shape)
         if lse is None:
-            lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-        return (rows, qp, _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev, (d.batch + 1,)),
-                _ptr(out, "out", torch.bfloat16, dev, shape), _ptr(lse, "lse", torch.float32, dev, shape[:2]), out, lse)
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=dev)
+            lp = lse.data_ptr()
+        else:
+            lp = _ptr(lse, "lse", torch.float32, dev, lse_shape)
+        return out, lse, qp, _ptr(cu_seqlens, "cu_seqlens", torch.int32, dev, cu_shape), op, lp, kv_shape
+
+    def _shapes_of(self, rows):
+        d = self.dims
+        return ((rows, d.num_q_heads, d.head_dim), (rows, d.num_q_heads), (d.batch + 1,),
+                (rows, d.num_kv_heads, d.head_dim))
 
     def check(self) -> int:
         """Waits for the current stream; the device status of the last call (binding.STATUS_NAMES)."""
@@ -241,12 +257,11 @@ class VerifyAttnQ8(_AttnQ8):
         return int(load_library().ls_verify_attn_q8_workspace_size(self._dims_ref, self._tree_ref))
 
     def __call__(self, q, cache, k_tree, v_tree, parent, cu_seqlens, out=None, lse=None):
-        rows, qp, cu, op, lp, out, lse = self._check(q, cache, cu_seqlens, out, lse)
-        dev, shape = self.device, (rows, self.dims.num_kv_heads, self.dims.head_dim)
-        _call(dev, self._name, load_library().ls_verify_attn_q8, qp, cache._ref,
-              _ptr(k_tree, "k_tree", torch.bfloat16, dev, shape), _ptr(v_tree, "v_tree", torch.bfloat16, dev, shape),
-              _ptr(parent, "tree_parent", torch.int32, dev, (rows,)), cu, self._tree_ref, op, lp, self._dims_ref,
-              self._ws_ptr, self.ws_bytes)
+        out, lse, qp, cu, op, lp, shape = self._begin(q, cache, cu_seqlens, out, lse)
+        dev = self.device
+        _call(dev, self._name, self._fn, qp, cache._ref, _ptr(k_tree, "k_tree", torch.bfloat16, dev, shape),
+              _ptr(v_tree, "v_tree", torch.bfloat16, dev, shape), _ptr(parent, "tree_parent", torch.int32, dev, shape[:1]),
+              cu, self._tree_ref, op, lp, self._dims_ref, self._ws_ptr, self.ws_bytes)
         return out, lse
 
 
@@ -265,9 +280,8 @@ class CrossAttnQ8(_AttnQ8):
         return int(load_library().ls_cross_attn_q8_workspace_size(self._dims_ref))
 
     def __call__(self, q, cache, cu_seqlens, out=None, lse=None):
-        _, qp, cu, op, lp, out, lse = self._check(q, cache, cu_seqlens, out, lse)
-        _call(self.device, self._name, load_library().ls_cross_attn_q8, qp, cache._ref, cu, op, lp, self._dims_ref,
-              self._ws_ptr, self.ws_bytes)
+        out, lse, qp, cu, op, lp, _ = self._begin(q, cache, cu_seqlens, out, lse)
+        _call(self.device, self._name, self._fn, qp, cache._ref, cu, op, lp, self._dims_ref, self._ws_ptr, self.ws_bytes)
         return out, lse
 
 
@@ -342,12 +356,12 @@ def tree_accept_sample(logits, uniform, tree_tokens, tree_parent, tree_size: int
             raise ValueError(f"{rows} rows of logits are not whole trees of {tree_size} nodes")
     tok = _ptr(tree_tokens, "tree_tokens", torch.int32, dev, (rows,))
     par = _ptr(tree_parent, "tree_parent", torch.int32, dev, (rows,))
-    # one allocation for the four results
-    node_token, accept_len, accept_path, next_token = torch.empty(
-        (rows + 2 * batch + batch * tree_size,), dtype=torch.int32, device=dev).split(
-        (rows, batch, batch * tree_size, batch))
+    node_token = torch.empty((rows,), dtype=torch.int32, device=dev)
+    accept_path = torch.empty((batch, tree_size), dtype=torch.int32, device=dev)
+    accept_len = torch.empty((batch,), dtype=torch.int32, device=dev)
+    next_token = torch.empty((batch,), dtype=torch.int32, device=dev)
     dims = binding.AcceptDims(batch, tree_size, vocab, kind)
     _call(dev, "ls_tree_accept_sample", load_library().ls_tree_accept_sample, logits.data_ptr(), u,
           ctypes.byref(opts), tok, par, trees, rows, node_token.data_ptr(), accept_len.data_ptr(),
           accept_path.data_ptr(), next_token.data_ptr(), ctypes.byref(dims))
-    return node_token, accept_len, accept_path.view(batch, tree_size), next_token
+    return node_token, accept_len, accept_path, next_token
