@@ -74,7 +74,9 @@ constexpr float kMaxX = 30.6f;  // exp(-30.6) is below half a unit
 constexpr int kPartBits = 15;
 constexpr int kMaxSeg = 1 << 17;
 constexpr int kLut = 1024;  // e^(-b / 32) * 2^43
-constexpr int kDataBytes = 76 * 1024;
+constexpr int kKeys = 6144;  // bins of the histogram over bf16 values
+constexpr int kKeysPer = kKeys / kThreads;
+constexpr int kDataBytes = 76 * 1024;  // of the row, in shared memory
 
 using u64 = unsigned long long;
 
@@ -97,6 +99,12 @@ struct Fast {
   uint32_t hist[kFine];  // later the sorted list (u64[kList])
   u64 list[kList];
 };
+struct Keys {
+  union {
+    uint32_t hist[kKeys];
+    double weight[kKeys / 2];  // later: of the bins kept
+  };
+};
 struct Slow {
   u64 hist[kBins];          // this CTA's measure of each bin
   uint32_t part[3][kBins];  // its parts while they are added up
@@ -118,10 +126,20 @@ struct Verdict {
   int ok, owner;
 };
 
+// What the histogram over bf16 values decides: `edge` is the last value kept, `m` of its
+// entries with it (each of weight w); ok = 0: nothing (values too small to have a bin).
+struct KeyVerdict {
+  u64 target, w;
+  float edge;
+  uint32_t m, bin;
+  int ok;
+};
+
 struct Shared {
   double lut[kLut];
   union {
     Fast f;
+    Keys k;
     Slow s;
   };
   u64 wsum[kWarps], scan[kWarps];
@@ -132,9 +150,10 @@ struct Shared {
   u64 last, before;
   Borders borders;
   Verdict verdict;
+  KeyVerdict keys;
   uint32_t lpart[3][kWarps], cpart[3][kWarps];  // kept weights of the list, by run of this CTA and by CTA
   uint32_t n_list, kmin, kmax;                  // listed entries; `select`: keys of the border bin
-  uint32_t bin, bins[3], in_range[2], cut;
+  uint32_t bin, bins[3], in_range[2], cut, tiny;
   uint32_t cwarp[kWarps];
   float fmax[kWarps], fmin[kWarps], fsum[kWarps];
   float top, low;
@@ -276,6 +295,10 @@ class Sampler {
     const float p = a_.top_p != nullptr ? a_.top_p[row_id_] : 1.0f;
     const uint32_t least = least_key(a_.min_p != nullptr ? a_.min_p[row_id_] : 0.0f, t);
     const float u = a_.uniform[row_id_];
+    if constexpr (!F32) {
+      if ((k > 0 || p < 1.0f) && resolve_keys(k, p, t, least, u)) return;
+      cl_.sync();  // the memory changes hands
+    }
     if (resolve(k, p, least, u)) return;
     cl_.sync();  // the memory changes hands
     Keep keep{0u, 0xffffffffu};
@@ -776,6 +799,288 @@ class Sampler {
         mine = cl_.map_shared_rank(&sh_, o.owner)->tot[0] + parts(sh_.cpart, o.owner);
       }
       sh_.verdict = o;
+    }
+  }
+
+  // ---- bf16 rows: one bin per value
+  //
+  // Logits of 8 significant bits have few values: those that weigh anything lie within
+  // [top - 31 t, top], some 6000 of them down to 2^-20. Bins for each, in falling order, make
+  // the histogram exact: thresholds and sums come from counts times weights, without a list,
+  // and what is left to do for the entries themselves is to add up the kept ones' weights by
+  // runs, from a table.
+  struct KeyMap {
+    int ptop, zero, neg0, least, count;  // bins: ptop - magnitude | zero | neg0 + magnitude
+    __device__ __forceinline__ int bin(uint32_t u) const {  // of a bf16's bits; not in [0, count): none
+      const int mag = (int)(u & 0x7fffu);
+      if (mag < least) return mag == 0 ? zero : -1;
+      return (u & 0x8000u) ? neg0 + mag : ptop - mag;
+    }
+    __device__ __forceinline__ float value(int b) const {
+      if (b == zero) return 0.f;
+      return b < zero ? __uint_as_float((uint32_t)(ptop - b) << 16) : -__uint_as_float((uint32_t)(b - neg0) << 16);
+    }
+  };
+  // The map for this row; false where its range of values has no room.
+  __device__ bool key_map(float t, KeyMap* k) const {
+    const float low = top_ - kMaxX * t;  // below it, weights are 0
+    if (!(low < top_) || top_ == INFINITY) return false;
+    const int last = low < 0.f ? (int)min(__float_as_uint(-low) >> 16, 0x7f7eu) + 1 : 0;  // largest magnitude below 0
+    if (top_ > 0.f) {
+      const int p = (int)(__float_as_uint(top_) >> 16);
+      // bins: p - least + 1, the zero, last - least + 1
+      const int least = max(1, last > 0 ? (p + last + 4 - kKeys) / 2 : p + 2 - kKeys);
+      if (least > p) return false;
+      const int zero = p - least + 1;
+      *k = KeyMap{p, zero, zero + 1 - least, least, last >= least ? zero + 2 - least + last : zero + 1};
+    } else if (top_ == 0.f) {
+      const int least = max(1, last + 2 - kKeys);
+      *k = KeyMap{-1, 0, 1 - least, least, last >= least ? 2 - least + last : 1};
+    } else {
+      const int p = (int)(__float_as_uint(-top_) >> 16);
+      *k = KeyMap{-1, -1, -p, p, last - p + 1};
+    }
+    return k->count <= kKeys && k->count > 0;
+  }
+
+  __device__ bool resolve_keys(int k, float p, float t, uint32_t least, float u) {
+    KeyMap map;
+    if (!(inv_f_ > 0.f && inv_f_ < INFINITY) || !key_map(t, &map)) return false;
+    uint32_t* hist = sh_.k.hist;
+    for (int i = tid_; i < kKeys / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid_ == 0) sh_.tiny = 0u;
+    __syncthreads();
+    bool tiny = false;  // an entry without a bin that weighs something
+    each([&](float x, uint32_t) {
+      const int b = map.bin(__float_as_uint(x) >> 16);
+      if ((uint32_t)b < (uint32_t)map.count)
+        atomicAdd(&hist[b], 1u);
+      else
+        tiny |= b == -1;
+    });
+    if (__any_sync(0xffffffffu, tiny) && lane_ == 0) sh_.tiny = 1u;
+    cl_.sync();
+    if (size_ > 1) {
+      const int share = kKeys / 4 / size_;
+      for (int i = rank_ * share + tid_; i < (rank_ + 1) * share; i += kThreads) {
+        uint4 v[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < size_) v[r] = reinterpret_cast<const uint4*>(cl_.map_shared_rank(&sh_, r)->k.hist)[i];
+#pragma unroll
+        for (int r = 1; r < kMaxCluster; ++r)
+          if (r < size_) {
+            v[0].x += v[r].x;
+            v[0].y += v[r].y;
+            v[0].z += v[r].z;
+            v[0].w += v[r].w;
+          }
+        reinterpret_cast<uint4*>(hist)[i] = v[0];
+      }
+      cl_.sync();
+    }
+    if (rank_ == 0) look_keys(map, (uint32_t)k, p, least, u);
+    cl_.sync();
+    const KeyVerdict o = cl_.map_shared_rank(&sh_, 0)->keys;
+    if (!o.ok) return false;
+    // weights of the bins kept whole, where the histogram was
+    const int whole = (int)o.bin;
+    const float least_f = least > 0u ? of_key(least) : -INFINITY;
+    for (int b = tid_; b < min(whole, kKeys / 2); b += kThreads) sh_.k.weight[b] = (double)weight(map.value(b));
+    __syncthreads();
+    const float edge = o.edge;
+    const uint32_t cut = edge >= least_f ? o.m : 0u;  // of the edge's own entries, the first `cut` are kept
+    auto weight_at = [&](float x) {
+      const int b = map.bin(__float_as_uint(x) >> 16);
+      return b < kKeys / 2 ? sh_.k.weight[b] : (double)weight(x);
+    };
+    double keep = 0.0;
+    uint32_t equal = 0;
+    each_vector([&](float (&x)[kPer], uint32_t) {
+      float most = x[0];
+#pragma unroll
+      for (int e = 1; e < kPer; ++e) most = fmaxf(most, x[e]);
+      if (!(most >= edge && most >= least_f)) return;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (x[e] > edge && x[e] >= least_f) keep += weight_at(x[e]);
+        equal += x[e] == edge ? 1u : 0u;
+      }
+    });
+    const u64 s_keep = warp_sum64((u64)keep);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane_ == 0) {
+      sh_.ws[0][warp_] = s_keep;
+      sh_.ws[1][warp_] = equal;
+    }
+    __syncthreads();
+    if (warp_ < 2) {
+      const u64 v = warp_sum64(lane_ < kWarps ? sh_.ws[warp_][lane_] : 0ull);
+      if (lane_ == 0) sh_.tot[warp_] = v;
+    }
+    cl_.sync();
+    // the CTA, the warp's run, and the part of it that the target falls in; `pre`: kept weight
+    // before it, `seen`: the edge's entries before it
+    auto kept_of = [&](u64 whole_w, u64 n, u64 seen) { return whole_w + (min(seen + n, (u64)cut) - min(seen, (u64)cut)) * o.w; };
+    u64 pre = 0, seen = 0;
+    int owner = -1;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      if (c >= size_ || owner >= 0) continue;
+      const Shared* q = cl_.map_shared_rank(&sh_, c);
+      const u64 n = q->tot[1], mine = kept_of(q->tot[0], n, seen);
+      if (o.target < pre + mine) {
+        owner = c;
+      } else {
+        pre += mine;
+        seen += n;
+      }
+    }
+    if (owner != rank_) return true;
+    int w = 0;
+    for (; w < kWarps - 1; ++w) {
+      const u64 mine = kept_of(sh_.ws[0][w], sh_.ws[1][w], seen);
+      if (o.target < pre + mine) break;
+      pre += mine;
+      seen += sh_.ws[1][w];
+    }
+    const int r0 = min(r_.n, w * run_), r1 = min(r_.n, r0 + run_);
+    const int sub = (run_ / 64 + kWarps - 1) / kWarps * 64;
+    const int i0 = min(r1, r0 + warp_ * sub), i1 = min(r1, i0 + sub);
+    auto whole_weight = [&](float x) { return x > edge && x >= least_f ? (u64)weight_at(x) : 0ull; };
+    u64 s = 0;
+    uint32_t n = 0;
+    for (int i = i0 + lane_; i < i1; i += 32) {
+      const float x = r_.one(i);
+      s += whole_weight(x);
+      n += x == edge ? 1u : 0u;
+    }
+    s = warp_sum64(s);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane_ == 0) {
+      sh_.scan[warp_] = s;
+      sh_.cwarp[warp_] = n;
+    }
+    __syncthreads();
+    for (int q = 0; q < warp_; ++q) {
+      pre += kept_of(sh_.scan[q], sh_.cwarp[q], seen);
+      seen += sh_.cwarp[q];
+    }
+    if (o.target < pre || o.target >= pre + kept_of(s, n, seen)) return true;
+    for (int i = i0; i < i1; i += 32) {
+      const float x = i + lane_ < i1 ? r_.one(i + lane_) : __uint_as_float(0x7fffffffu);
+      const uint32_t same = __ballot_sync(0xffffffffu, x == edge);
+      const u64 at = seen + __popc(same & ((1u << lane_) - 1u));
+      const u64 mine = x == edge ? (at < cut ? o.w : 0ull) : whole_weight(x);
+      const u64 upto = pre + warp_scan(mine, lane_);
+      if (o.target < upto && o.target >= upto - mine) a_.out[row_id_] = lo_ + i + lane_;
+      pre = __shfl_sync(0xffffffffu, upto, 31);
+      if (o.target < pre) break;
+      seen += __popc(same);
+    }
+    return true;
+  }
+
+  // Rank 0: the summed histogram's verdict, into its sh_.keys.
+  __device__ void look_keys(const KeyMap& map, uint32_t k, float p, uint32_t least, float u) {
+    uint32_t c[kKeysPer], tiny = 0;
+#pragma unroll
+    for (int e = 0; e < kKeysPer / 4; ++e) {
+      const int i = tid_ * (kKeysPer / 4) + e;
+      const Shared* o = cl_.map_shared_rank(&sh_, i / (kKeys / 4 / size_));
+      const uint4 v = reinterpret_cast<const uint4*>(o->k.hist)[i];
+      c[4 * e] = v.x;
+      c[4 * e + 1] = v.y;
+      c[4 * e + 2] = v.z;
+      c[4 * e + 3] = v.w;
+    }
+    for (int r = 0; r < size_; ++r) tiny |= cl_.map_shared_rank(&sh_, r)->tiny;
+    const int b0 = kKeysPer * tid_;
+    // top-k's border: bins before bk are kept whole, `room` entries of it
+    uint32_t own = 0;
+#pragma unroll
+    for (int e = 0; e < kKeysPer; ++e) own += c[e];
+    const uint32_t inc = warp_scan(own, lane_);
+    if (lane_ == 31) sh_.cwarp[warp_] = inc;
+    if (tid_ == 0) {
+      sh_.keys.ok = 0;
+      sh_.bin = kKeys;  // none: the entries with a weight are fewer
+      sh_.cut = 0u;
+    }
+    __syncthreads();
+    uint32_t before = inc - own;
+    for (int w = 0; w < warp_; ++w) before += sh_.cwarp[w];
+    if (k > before && k <= before + own) {
+      uint32_t at = before;
+      int e = 0;
+#pragma unroll
+      for (int q = 0; q < kKeysPer; ++q)
+        if (q == e && at + c[q] < k) {
+          at += c[q];
+          ++e;
+        }
+      sh_.bin = (uint32_t)(b0 + e);
+      sh_.cut = k - at;
+    }
+    __syncthreads();
+    const int bk = (int)sh_.bin;
+    const uint32_t room = sh_.cut;
+#pragma unroll
+    for (int e = 0; e < kKeysPer; ++e) c[e] = b0 + e < bk ? c[e] : b0 + e == bk ? room : 0u;
+    // weights: of the thread's bins, and those before them; with min-p, of the ones it keeps
+    const float least_f = least > 0u ? of_key(least) : -INFINITY;
+    u64 mass = 0;
+#pragma unroll
+    for (int e = 0; e < kKeysPer; ++e)
+      if (c[e]) mass += c[e] * weight(map.value(b0 + e));
+    const u64 minc = warp_scan(mass, lane_);
+    if (lane_ == 31) sh_.scan[warp_] = minc;
+    __syncthreads();
+    u64 mbefore = minc - mass, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp_) mbefore += sh_.scan[w];
+      all += sh_.scan[w];
+    }
+    u64 goal = all;  // the border holds the goal-th unit of weight: the last kept
+    if (p < 1.0f) {
+      const double g = ceil((double)p * (double)all);
+      goal = g >= 1.0 ? min((u64)g, all) : 1ull;
+    }
+    if (goal > mbefore && goal <= mbefore + mass) {
+      u64 at = mbefore;
+      bool found = false;
+#pragma unroll
+      for (int q = 0; q < kKeysPer; ++q) {
+        if (found || !c[q]) continue;
+        const u64 wq = weight(map.value(b0 + q));
+        if (at + c[q] * wq >= goal) {
+          found = true;
+          sh_.keys.edge = map.value(b0 + q);
+          sh_.keys.bin = (uint32_t)(b0 + q);
+          sh_.keys.w = wq;
+          sh_.keys.m = (uint32_t)((goal - at + wq - 1) / wq);
+          sh_.total = at + (u64)sh_.keys.m * wq;  // kept, but for min-p
+        } else {
+          at += c[q] * wq;
+        }
+      }
+    }
+    __syncthreads();
+    u64 z = sh_.total;
+    if (least > 0u && sh_.keys.edge < least_f) {  // min-p ends before the border
+      u64 kept = 0;
+#pragma unroll
+      for (int e = 0; e < kKeysPer; ++e)
+        if (c[e] && map.value(b0 + e) >= least_f) kept += c[e] * weight(map.value(b0 + e));
+      kept = warp_sum64(kept);
+      if (lane_ == 0) sh_.wsum[warp_] = kept;
+      __syncthreads();
+      z = 0;
+      for (int w = 0; w < kWarps; ++w) z += sh_.wsum[w];
+    }
+    if (tid_ == 0) {
+      sh_.keys.target = target_of(u, z);
+      sh_.keys.ok = tiny == 0u ? 1 : 0;
     }
   }
 
