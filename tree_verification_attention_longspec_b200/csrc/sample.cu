@@ -199,6 +199,9 @@ struct Row {
       }
     }
   }
+  __device__ __forceinline__ uint4 words(int i) const {
+    return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(s) + (F32 ? 4 : 2) * i);
+  }
   __device__ __forceinline__ float one(int i) const {
     if (i >= cap) return load(i);
     if constexpr (F32)
@@ -230,6 +233,27 @@ __device__ __forceinline__ void add_below(double& sum, double w, float a, float 
   asm("{\n\t.reg .pred p;\n\tsetp.lt.f32 p, %2, %3;\n\tsetp.ge.and.f32 p, %4, %5, p;\n\t@p add.rn.f64 %0, %0, %1;\n\t}"
       : "+d"(sum)
       : "d"(w), "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
+// Packed bf16 pairs, NaN skipped.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// sum += the double at shared address `at`, where a > b and a >= c.
+__device__ __forceinline__ void add_above(double& sum, uint32_t at, float a, float b, float c) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .f64 v;\n\tmov.f64 v, 0d0000000000000000;\n\tsetp.gt.f32 p, %2, %3;\n\t"
+      "setp.ge.and.f32 p, %2, %4, p;\n\t@p ld.shared.f64 v, [%1];\n\tadd.rn.f64 %0, %0, v;\n\t}"
+      : "+d"(sum)
+      : "r"(at), "f"(a), "f"(b), "f"(c)
+      : "memory");
 }
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
@@ -367,6 +391,13 @@ class Sampler {
     return min(key, most);
   }
 
+  // f(16 bytes) over this warp's run where they lie in shared memory, g(value) over the rest
+  template <class F, class G>
+  __device__ __forceinline__ void each_words(F f, G g) const {
+    const int whole = w0_ + max(0, min(w1_, r_.cap) - w0_) / kPer * kPer;
+    for (int i = w0_ + kPer * lane_; i < whole; i += 32 * kPer) f(r_.words(i));
+    for (int i = whole + lane_; i < w1_; i += 32) g(r_.one(i));
+  }
   // f(values, entry of the first) over this warp's run, 16 bytes a lane and step (NaN, which
   // weighs nothing, beyond its end)
   template <class F>
@@ -419,10 +450,23 @@ class Sampler {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     float mx = -INFINITY, mn = INFINITY;
-    each([&](float x, uint32_t) {
+    auto take = [&](float x) {
       mx = fmaxf(mx, x);
       mn = fminf(mn, x);
-    });
+    };
+    if constexpr (F32) {
+      each([&](float x, uint32_t) { take(x); });
+    } else {
+      uint32_t m2 = 0xff80ff80u, n2 = 0x7f807f80u;  // -inf, +inf
+      each_words(
+          [&](const uint4& v) {
+            m2 = max_bf16x2(m2, max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w)));
+            n2 = min_bf16x2(n2, min_bf16x2(min_bf16x2(v.x, v.y), min_bf16x2(v.z, v.w)));
+          },
+          take);
+      mx = fmaxf(mx, fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u)));
+      mn = fminf(mn, fminf(__uint_as_float(n2 << 16), __uint_as_float(n2 & 0xffff0000u)));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -816,6 +860,11 @@ class Sampler {
       if (mag < least) return mag == 0 ? zero : -1;
       return (u & 0x8000u) ? neg0 + mag : ptop - mag;
     }
+    // the same of bits whose magnitude is at least `least`
+    __device__ __forceinline__ int large_bin(uint32_t u) const {
+      const int neg = (int)(u << 16) >> 31;
+      return ((int)(u & 0x7fffu) ^ ~neg) + (neg ? neg0 : ptop + 1);
+    }
     __device__ __forceinline__ float value(int b) const {
       if (b == zero) return 0.f;
       return b < zero ? __uint_as_float((uint32_t)(ptop - b) << 16) : -__uint_as_float((uint32_t)(b - neg0) << 16);
@@ -851,13 +900,35 @@ class Sampler {
     if (tid_ == 0) sh_.tiny = 0u;
     __syncthreads();
     bool tiny = false;  // an entry without a bin that weighs something
-    each([&](float x, uint32_t) {
-      const int b = map.bin(__float_as_uint(x) >> 16);
+    auto count = [&](uint32_t bits) {
+      const int b = map.bin(bits);
       if ((uint32_t)b < (uint32_t)map.count)
         atomicAdd(&hist[b], 1u);
       else
         tiny |= b == -1;
-    });
+    };
+    each_words(
+        [&](const uint4& v) {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t small = 0x7fff7fffu;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) small = __vminu2(small, w[e] & 0x7fff7fffu);
+          if (min(small & 0xffffu, small >> 16) < (uint32_t)map.least) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              count(w[e] & 0xffffu);
+              count(w[e] >> 16);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int a = map.large_bin(w[e] & 0xffffu), b = map.large_bin(w[e] >> 16);
+              if ((uint32_t)a < (uint32_t)map.count) atomicAdd(&hist[a], 1u);
+              if ((uint32_t)b < (uint32_t)map.count) atomicAdd(&hist[b], 1u);
+            }
+          }
+        },
+        [&](float x) { count(__float_as_uint(x) >> 16); });
     if (__any_sync(0xffffffffu, tiny) && lane_ == 0) sh_.tiny = 1u;
     cl_.sync();
     if (size_ > 1) {
@@ -896,17 +967,35 @@ class Sampler {
     };
     double keep = 0.0;
     uint32_t equal = 0;
-    each_vector([&](float (&x)[kPer], uint32_t) {
-      float most = x[0];
+    auto add = [&](float x) {
+      if (x > edge && x >= least_f) keep += weight_at(x);
+      equal += x == edge ? 1u : 0u;
+    };
+    const uint32_t table = (uint32_t)__cvta_generic_to_shared(sh_.k.weight);
+    const float low = fmaxf(edge, least_f);
+    each_words(
+        [&](const uint4& v) {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t m2 = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
+          if (!(fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u)) >= low)) return;
+          if (whole > kKeys / 2 || edge <= 0.f) {  // past the table, or values around 0 among the kept
 #pragma unroll
-      for (int e = 1; e < kPer; ++e) most = fmaxf(most, x[e]);
-      if (!(most >= edge && most >= least_f)) return;
+            for (int e = 0; e < 4; ++e) {
+              add(__uint_as_float(w[e] << 16));
+              add(__uint_as_float(w[e] & 0xffff0000u));
+            }
+          } else {  // kept values are positive: a bin is the distance of their bits from the largest's
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        if (x[e] > edge && x[e] >= least_f) keep += weight_at(x[e]);
-        equal += x[e] == edge ? 1u : 0u;
-      }
-    });
+            for (int e = 0; e < 4; ++e) {
+              const float x = __uint_as_float(w[e] << 16), y = __uint_as_float(w[e] & 0xffff0000u);
+              add_above(keep, table + 8u * (uint32_t)(map.ptop - (int)(w[e] & 0xffffu)), x, edge, least_f);
+              add_above(keep, table + 8u * (uint32_t)(map.ptop - (int)(w[e] >> 16)), y, edge, least_f);
+              equal += x == edge ? 1u : 0u;
+              equal += y == edge ? 1u : 0u;
+            }
+          }
+        },
+        add);
     const u64 s_keep = warp_sum64((u64)keep);
     equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane_ == 0) {
@@ -994,7 +1083,9 @@ class Sampler {
       c[4 * e + 2] = v.z;
       c[4 * e + 3] = v.w;
     }
-    for (int r = 0; r < size_; ++r) tiny |= cl_.map_shared_rank(&sh_, r)->tiny;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < size_) tiny |= cl_.map_shared_rank(&sh_, r)->tiny;
     const int b0 = kKeysPer * tid_;
     // top-k's border: bins before bk are kept whole, `room` entries of it
     uint32_t own = 0;
@@ -1030,9 +1121,13 @@ class Sampler {
     // weights: of the thread's bins, and those before them; with min-p, of the ones it keeps
     const float least_f = least > 0u ? of_key(least) : -INFINITY;
     u64 mass = 0;
+    double wt[kKeysPer];
 #pragma unroll
-    for (int e = 0; e < kKeysPer; ++e)
-      if (c[e]) mass += c[e] * weight(map.value(b0 + e));
+    for (int e = 0; e < kKeysPer; ++e) {
+      const float x = map.value(b0 + e);
+      wt[e] = c[e] ? (double)weight(x) : 0.0;
+      mass += c[e] * (u64)wt[e];
+    }
     const u64 minc = warp_scan(mass, lane_);
     if (lane_ == 31) sh_.scan[warp_] = minc;
     __syncthreads();
@@ -1052,7 +1147,7 @@ class Sampler {
 #pragma unroll
       for (int q = 0; q < kKeysPer; ++q) {
         if (found || !c[q]) continue;
-        const u64 wq = weight(map.value(b0 + q));
+        const u64 wq = (u64)wt[q];
         if (at + c[q] * wq >= goal) {
           found = true;
           sh_.keys.edge = map.value(b0 + q);
@@ -1071,7 +1166,7 @@ class Sampler {
       u64 kept = 0;
 #pragma unroll
       for (int e = 0; e < kKeysPer; ++e)
-        if (c[e] && map.value(b0 + e) >= least_f) kept += c[e] * weight(map.value(b0 + e));
+        if (map.value(b0 + e) >= least_f) kept += c[e] * (u64)wt[e];
       kept = warp_sum64(kept);
       if (lane_ == 0) sh_.wsum[warp_] = kept;
       __syncthreads();
