@@ -74,8 +74,9 @@ constexpr float kMaxX = 30.6f;  // exp(-30.6) is below half a unit
 constexpr int kPartBits = 15;
 constexpr int kMaxSeg = 1 << 17;
 constexpr int kLut = 1024;  // e^(-b / 32) * 2^43
-constexpr int kKeys = 6144;  // bins of the histogram over bf16 values
-constexpr int kKeysPer = kKeys / kThreads;
+constexpr int kKeys = 4096;  // bins of the histogram over bf16 values
+constexpr int kKeysPer = kKeys / kThreads;  // of a group; the cluster has a group for each thread of a CTA
+constexpr int kTable = kKeys / 2;           // weights that fit the histogram's place
 constexpr int kDataBytes = 76 * 1024;  // of the row, in shared memory
 
 using u64 = unsigned long long;
@@ -102,8 +103,10 @@ struct Fast {
 struct Keys {
   union {
     uint32_t hist[kKeys];
-    double weight[kKeys / 2];  // later: of the bins kept
+    double weight[kTable];  // later: of the bins kept
   };
+  u64 mass[kThreads];  // of this CTA's groups of bins
+  uint32_t count[kThreads];
 };
 struct Slow {
   u64 hist[kBins];          // this CTA's measure of each bin
@@ -153,7 +156,8 @@ struct Shared {
   KeyVerdict keys;
   uint32_t lpart[3][kWarps], cpart[3][kWarps];  // kept weights of the list, by run of this CTA and by CTA
   uint32_t n_list, kmin, kmax;                  // listed entries; `select`: keys of the border bin
-  uint32_t bin, bins[3], in_range[2], cut, tiny;
+  uint32_t bin, bins[3], in_range[2], cut;
+  u64 tiny;  // weight of the entries without a bin
   uint32_t cwarp[kWarps];
   float fmax[kWarps], fmin[kWarps], fsum[kWarps];
   float top, low;
@@ -849,10 +853,11 @@ class Sampler {
   // ---- bf16 rows: one bin per value
   //
   // Logits of 8 significant bits have few values: those that weigh anything lie within
-  // [top - 31 t, top], some 6000 of them down to 2^-20. Bins for each, in falling order, make
+  // [top - 31 t, top], some 4000 of them down to 2^-13. Bins for each, in falling order, make
   // the histogram exact: thresholds and sums come from counts times weights, without a list,
   // and what is left to do for the entries themselves is to add up the kept ones' weights by
-  // runs, from a table.
+  // runs, from a table. Smaller magnitudes have no bin: their few entries' weights are added
+  // up one by one, which does as long as the threshold lies above 0; else `resolve` decides.
   struct KeyMap {
     int ptop, zero, neg0, least, count;  // bins: ptop - magnitude | zero | neg0 + magnitude
     __device__ __forceinline__ int bin(uint32_t u) const {  // of a bf16's bits; not in [0, count): none
@@ -897,15 +902,15 @@ class Sampler {
     if (!(inv_f_ > 0.f && inv_f_ < INFINITY) || !key_map(t, &map)) return false;
     uint32_t* hist = sh_.k.hist;
     for (int i = tid_; i < kKeys / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid_ == 0) sh_.tiny = 0u;
+    if (tid_ == 0) sh_.tiny = 0ull;
     __syncthreads();
-    bool tiny = false;  // an entry without a bin that weighs something
+    u64 tiny = 0;
     auto count = [&](uint32_t bits) {
       const int b = map.bin(bits);
       if ((uint32_t)b < (uint32_t)map.count)
         atomicAdd(&hist[b], 1u);
-      else
-        tiny |= b == -1;
+      else if (b == -1)
+        tiny += weight(__uint_as_float(bits << 16));
     };
     each_words(
         [&](const uint4& v) {
@@ -929,7 +934,7 @@ class Sampler {
           }
         },
         [&](float x) { count(__float_as_uint(x) >> 16); });
-    if (__any_sync(0xffffffffu, tiny) && lane_ == 0) sh_.tiny = 1u;
+    if (tiny) atomicAdd(&sh_.tiny, tiny);
     cl_.sync();
     if (size_ > 1) {
       const int share = kKeys / 4 / size_;
@@ -948,8 +953,27 @@ class Sampler {
           }
         reinterpret_cast<uint4*>(hist)[i] = v[0];
       }
-      cl_.sync();
+      __syncthreads();
     }
+    {  // its groups' counts and weights, size_ threads a group
+      const int g = tid_ / size_, b0 = (rank_ * (kThreads / size_) + g) * kKeysPer;
+      u64 mass = 0;
+      uint32_t cnt = 0;
+      for (int e = tid_ % size_; e < kKeysPer; e += size_) {
+        const uint32_t c = hist[b0 + e];
+        cnt += c;
+        if (c) mass += c * weight(map.value(b0 + e));
+      }
+      for (int o = size_ / 2; o > 0; o /= 2) {
+        cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+        mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      }
+      if (tid_ % size_ == 0) {
+        sh_.k.mass[g] = mass;
+        sh_.k.count[g] = cnt;
+      }
+    }
+    cl_.sync();
     if (rank_ == 0) look_keys(map, (uint32_t)k, p, least, u);
     cl_.sync();
     const KeyVerdict o = cl_.map_shared_rank(&sh_, 0)->keys;
@@ -957,13 +981,13 @@ class Sampler {
     // weights of the bins kept whole, where the histogram was
     const int whole = (int)o.bin;
     const float least_f = least > 0u ? of_key(least) : -INFINITY;
-    for (int b = tid_; b < min(whole, kKeys / 2); b += kThreads) sh_.k.weight[b] = (double)weight(map.value(b));
+    for (int b = tid_; b < min(whole, kTable); b += kThreads) sh_.k.weight[b] = (double)weight(map.value(b));
     __syncthreads();
     const float edge = o.edge;
     const uint32_t cut = edge >= least_f ? o.m : 0u;  // of the edge's own entries, the first `cut` are kept
     auto weight_at = [&](float x) {
       const int b = map.bin(__float_as_uint(x) >> 16);
-      return b < kKeys / 2 ? sh_.k.weight[b] : (double)weight(x);
+      return b < kTable ? sh_.k.weight[b] : (double)weight(x);
     };
     double keep = 0.0;
     uint32_t equal = 0;
@@ -978,7 +1002,7 @@ class Sampler {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           const uint32_t m2 = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
           if (!(fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u)) >= low)) return;
-          if (whole > kKeys / 2 || edge <= 0.f) {  // past the table, or values around 0 among the kept
+          if (whole > kTable || edge <= 0.f) {  // past the table, or values around 0 among the kept
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               add(__uint_as_float(w[e] << 16));
@@ -1070,68 +1094,51 @@ class Sampler {
     return true;
   }
 
-  // Rank 0: the summed histogram's verdict, into its sh_.keys.
+  // Rank 0: the summed histogram's verdict, into its sh_.keys. Thread t has group t.
   __device__ void look_keys(const KeyMap& map, uint32_t k, float p, uint32_t least, float u) {
-    uint32_t c[kKeysPer], tiny = 0;
-#pragma unroll
-    for (int e = 0; e < kKeysPer / 4; ++e) {
-      const int i = tid_ * (kKeysPer / 4) + e;
-      const Shared* o = cl_.map_shared_rank(&sh_, i / (kKeys / 4 / size_));
-      const uint4 v = reinterpret_cast<const uint4*>(o->k.hist)[i];
-      c[4 * e] = v.x;
-      c[4 * e + 1] = v.y;
-      c[4 * e + 2] = v.z;
-      c[4 * e + 3] = v.w;
-    }
+    const int groups = kThreads / size_, b0 = kKeysPer * tid_;  // of a CTA; the group's first bin
+    const Shared* o = cl_.map_shared_rank(&sh_, tid_ / groups);
+    const uint32_t own = o->k.count[tid_ % groups];
+    u64 mass = o->k.mass[tid_ % groups];
+    u64 tiny = 0;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
-      if (r < size_) tiny |= cl_.map_shared_rank(&sh_, r)->tiny;
-    const int b0 = kKeysPer * tid_;
+      if (r < size_) tiny += cl_.map_shared_rank(&sh_, r)->tiny;
+    auto count_of = [&](int e) { return o->k.hist[b0 + e]; };
     // top-k's border: bins before bk are kept whole, `room` entries of it
-    uint32_t own = 0;
-#pragma unroll
-    for (int e = 0; e < kKeysPer; ++e) own += c[e];
-    const uint32_t inc = warp_scan(own, lane_);
-    if (lane_ == 31) sh_.cwarp[warp_] = inc;
-    if (tid_ == 0) {
-      sh_.keys.ok = 0;
-      sh_.bin = kKeys;  // none: the entries with a weight are fewer
-      sh_.cut = 0u;
-    }
-    __syncthreads();
-    uint32_t before = inc - own;
-    for (int w = 0; w < warp_; ++w) before += sh_.cwarp[w];
-    if (k > before && k <= before + own) {
-      uint32_t at = before;
-      int e = 0;
-#pragma unroll
-      for (int q = 0; q < kKeysPer; ++q)
-        if (q == e && at + c[q] < k) {
-          at += c[q];
-          ++e;
+    int bk = kKeys;  // none: the entries with a bin are fewer
+    uint32_t room = 0;
+    if (k > 0) {
+      const uint32_t inc = warp_scan(own, lane_);
+      if (lane_ == 31) sh_.cwarp[warp_] = inc;
+      if (tid_ == 0) sh_.bin = kKeys;
+      __syncthreads();
+      uint32_t before = inc - own;
+      for (int w = 0; w < warp_; ++w) before += sh_.cwarp[w];
+      if (k > before && k <= before + own) {  // this thread's group has it
+        int e = 0;
+        mass = 0;
+        for (;; ++e) {
+          const uint32_t c = count_of(e);
+          if (before + c >= k) break;
+          before += c;
+          if (c) mass += c * weight(map.value(b0 + e));
         }
-      sh_.bin = (uint32_t)(b0 + e);
-      sh_.cut = k - at;
+        mass += (k - before) * weight(map.value(b0 + e));
+        sh_.bin = (uint32_t)(b0 + e);
+        sh_.cut = k - before;
+      }
+      __syncthreads();
+      bk = (int)sh_.bin;
+      room = sh_.cut;
+      if (b0 > bk) mass = 0;
     }
-    __syncthreads();
-    const int bk = (int)sh_.bin;
-    const uint32_t room = sh_.cut;
-#pragma unroll
-    for (int e = 0; e < kKeysPer; ++e) c[e] = b0 + e < bk ? c[e] : b0 + e == bk ? room : 0u;
-    // weights: of the thread's bins, and those before them; with min-p, of the ones it keeps
-    const float least_f = least > 0u ? of_key(least) : -INFINITY;
-    u64 mass = 0;
-    double wt[kKeysPer];
-#pragma unroll
-    for (int e = 0; e < kKeysPer; ++e) {
-      const float x = map.value(b0 + e);
-      wt[e] = c[e] ? (double)weight(x) : 0.0;
-      mass += c[e] * (u64)wt[e];
-    }
+    if (bk < map.zero) tiny = 0;  // top-k ends above them
     const u64 minc = warp_scan(mass, lane_);
     if (lane_ == 31) sh_.scan[warp_] = minc;
+    if (tid_ == 0) sh_.keys.ok = 0;
     __syncthreads();
-    u64 mbefore = minc - mass, all = 0;
+    u64 mbefore = minc - mass, all = tiny;
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp_) mbefore += sh_.scan[w];
       all += sh_.scan[w];
@@ -1143,40 +1150,46 @@ class Sampler {
     }
     if (goal > mbefore && goal <= mbefore + mass) {
       u64 at = mbefore;
-      bool found = false;
-#pragma unroll
-      for (int q = 0; q < kKeysPer; ++q) {
-        if (found || !c[q]) continue;
-        const u64 wq = (u64)wt[q];
-        if (at + c[q] * wq >= goal) {
-          found = true;
-          sh_.keys.edge = map.value(b0 + q);
-          sh_.keys.bin = (uint32_t)(b0 + q);
-          sh_.keys.w = wq;
-          sh_.keys.m = (uint32_t)((goal - at + wq - 1) / wq);
-          sh_.total = at + (u64)sh_.keys.m * wq;  // kept, but for min-p
-        } else {
-          at += c[q] * wq;
+      for (int e = 0; e < kKeysPer; ++e) {
+        const int b = b0 + e;
+        const uint32_t c = b < bk ? count_of(e) : b == bk ? room : 0u;
+        const u64 w = c ? weight(map.value(b)) : 0ull;
+        if (at + c * w < goal) {
+          at += c * w;
+          continue;
         }
+        sh_.keys.edge = map.value(b);
+        sh_.keys.bin = (uint32_t)b;
+        sh_.keys.w = w;
+        sh_.keys.m = (uint32_t)((goal - at + w - 1) / w);
+        sh_.total = at + (u64)sh_.keys.m * w;  // kept, but for min-p
+        // entries without a bin lie among those of the zero: they do not matter above it
+        sh_.keys.ok = tiny == 0ull || b < map.zero ? 1 : 0;
+        break;
       }
     }
     __syncthreads();
+    if (!sh_.keys.ok) return;
     u64 z = sh_.total;
-    if (least > 0u && sh_.keys.edge < least_f) {  // min-p ends before the border
+    const float least_f = least > 0u ? of_key(least) : -INFINITY;
+    if (sh_.keys.edge < least_f) {  // min-p ends before the border
       u64 kept = 0;
-#pragma unroll
-      for (int e = 0; e < kKeysPer; ++e)
-        if (map.value(b0 + e) >= least_f) kept += c[e] * (u64)wt[e];
+      if (map.value(b0) >= least_f) {
+        if (map.value(b0 + kKeysPer - 1) >= least_f)
+          kept = mass;
+        else
+          for (int e = 0; e < kKeysPer && map.value(b0 + e) >= least_f; ++e) {
+            const uint32_t c = count_of(e);
+            if (c) kept += c * weight(map.value(b0 + e));
+          }
+      }
       kept = warp_sum64(kept);
       if (lane_ == 0) sh_.wsum[warp_] = kept;
       __syncthreads();
       z = 0;
       for (int w = 0; w < kWarps; ++w) z += sh_.wsum[w];
     }
-    if (tid_ == 0) {
-      sh_.keys.target = target_of(u, z);
-      sh_.keys.ok = tiny == 0u ? 1 : 0;
-    }
+    if (tid_ == 0) sh_.keys.target = target_of(u, z);
   }
 
   // The row's token, by way of the list; false where the list does not hold the border (then
