@@ -760,14 +760,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         const int tb = j % kTables;
         // the block's scales first (they came long ago), then its scores
         float ck[kGroups], cm[kGroups];
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->table_full[tb], (j / kTables) & 1, abort, wait_ns));
+        const bool scaled = mbar_wait_bounded(&bars->table_full[tb], (j / kTables) & 1, abort, wait_ns);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           // not 0 (a row or a block of zeros), so that a masked score stays -inf
           ck[g] = fmaxf(bars->kc[tb][g] * cs, 1.17549435e-38f);
           cm[g] = bars->lv[tb][g];
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&bars->s_full[t], i & 1, abort, wait_ns));
+        ok = __all_sync(0xffffffffu, scaled && mbar_wait_bounded(&bars->s_full[t], i & 1, abort, wait_ns));
         if (!ok) break;
         tc_fence_after_sync();
         int shift = 0;  // masked leading columns (this row)
