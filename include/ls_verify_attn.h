@@ -420,7 +420,7 @@ LS_API int ls_cross_attn_q8(const void* q, const ls_kv_q8* kv, const int32_t* cu
  * Tokens past max_pages_per_seq * page_size are dropped. No other row is touched.
  *
  *   cu_seqlens      device int32 [B+1]: lengths before the call
- *   cu_seqlens_out  device int32 [B+1], not overlapping cu_seqlens, or NULL: written with
+ *   cu_seqlens_out  device int32 [B+1], overlapping no other array, or NULL: written with
  *                   the lengths after it (dropped tokens not counted)
  *   dims            batch, num_kv_heads, head_dim (and tree_size for the commit) are used
  * Returns LS_OK, LS_ERR_INVALID_ARG, LS_ERR_UNSUPPORTED or LS_ERR_CUDA; asynchronous on `stream`.
@@ -474,8 +474,8 @@ LS_API int ls_sample(const void* logits, int64_t row_stride, const float* unifor
  *   uniform      device fp32 [N], opts: arrays of N values
  *   node_token   device int32 [N], written: the token drawn at every node
  *   accept_path  [B, T]: the entries after the path are written as -1
- * and no workspace. The nodes' rows of logits are dense. LS_ERR_UNSUPPORTED: tree_size > 128
- * or vocab > 2^20.
+ * and no workspace. The nodes' rows of logits are dense; outputs overlap no other array.
+ * LS_ERR_UNSUPPORTED: tree_size > 128 or vocab > 2^20.
  */
 LS_API int ls_tree_accept_sample(const void* logits, const float* uniform, const ls_sample_opts* opts,
                                  const int32_t* tree_tokens, const int32_t* tree_parent, const int32_t* cu_tree,

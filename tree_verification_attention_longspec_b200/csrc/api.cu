@@ -538,6 +538,10 @@ int run_q8(const void* q, const ls_kv_q8* kv, const void* k_tree, const void* v_
   return run_combine(cu_seqlens, out, lse, dims, workspace, workspace_bytes, stream, with_tree, tree, &p);
 }
 
+bool overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+  return a != nullptr && b != nullptr && a < b + nb && b < a + na;
+}
+
 // What both writers of the cache share; arguments of the rows' source already checked.
 int run_append(ls::AppendArgs& a, const void* k_new, const void* v_new, const int32_t* cu_seqlens,
                int32_t* cu_seqlens_out, const ls_kv_q8* kv, const ls_verify_dims* dims, int64_t rows, int32_t max_new,
@@ -547,9 +551,11 @@ int run_append(ls::AppendArgs& a, const void* k_new, const void* v_new, const in
   if (cu_seqlens == nullptr || !aligned4(cu_seqlens) || !aligned4(cu_seqlens_out)) return LS_ERR_INVALID_ARG;
   if (rows > 0 && max_new > 0 && (k_new == nullptr || v_new == nullptr)) return LS_ERR_INVALID_ARG;
   if (!aligned16(k_new) || !aligned16(v_new)) return LS_ERR_INVALID_ARG;
-  // the lengths are read while the new ones are written
-  if (cu_seqlens_out != nullptr && cu_seqlens_out <= cu_seqlens + dims->batch &&
-      cu_seqlens <= cu_seqlens_out + dims->batch)
+  // the lengths, old and appended, are read while the new ones are written
+  const int64_t B = dims->batch, T = dims->tree_size;
+  if (overlap(cu_seqlens_out, B + 1, cu_seqlens, B + 1) || overlap(cu_seqlens_out, B + 1, a.cu_new, B + 1) ||
+      overlap(cu_seqlens_out, B + 1, a.cu_tree, B + 1) || overlap(cu_seqlens_out, B + 1, a.accept_len, B) ||
+      overlap(cu_seqlens_out, B + 1, a.accept_path, B * T))
     return LS_ERR_INVALID_ARG;
   int sms = 0, major = 0;
   const int rd = device_info(&sms, &major);
@@ -566,9 +572,11 @@ int run_append(ls::AppendArgs& a, const void* k_new, const void* v_new, const in
   a.rows = (int32_t)rows;
   // a sequence cannot append more than its table has room for
   a.max_new = (int32_t)std::min<int64_t>(max_new, (int64_t)kv->max_pages_per_seq * kv->page_size);
-  // n tokens touch at most (n - 1) / scale_block + 2 blocks, each sequence's and in all
+  // n tokens touch at most (n - 1) / scale_block + 2 blocks, each sequence's, and where the
+  // rows are packed, in all (a path may be longer than its tree: its other entries are skipped)
   const int64_t each = a.max_new > 0 ? (a.max_new - 1) / kv->scale_block + 2 : 0;
-  a.blocks = std::min<int64_t>(a.B * each, rows / kv->scale_block + 2ll * a.B);
+  a.blocks = a.B * each;
+  if (a.cu_new != nullptr) a.blocks = std::min<int64_t>(a.blocks, rows / kv->scale_block + 2ll * a.B);
   (void)cudaGetLastError();
   return ls::launch_q8_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LS_OK : LS_ERR_CUDA;
 }

@@ -12,18 +12,24 @@
 //
 // Decoding and small trees read each cached byte for few rows: HBM bounds them, and what
 // keeps HBM busy is bytes in flight. Every warp streams its own keys, 16 at a step, through
-// its own ring in shared memory (cp.async, five steps ahead: 20 KB a warp, 160 KB an SM at
-// d = 128; no barrier but the warp's own), converts them in registers and feeds mma.sync
-// with the cache as the A operand: S^T = K Q^T with 16 keys
-// by 8 rows, O^T += V^T P^T with 16 dimensions by 8 rows, so that 8 rows cost half of what
-// a 16-row A operand would. The order of d inside a K step and of V's rows is free, and is
-// chosen so that a lane's operands are contiguous bytes: 32 of each of its two keys, 16 of
-// each of its four values (byte pairs of two keys by PRMT). P^T comes out of S^T's
-// accumulators by movmatrix. (mma.sync: with 8 to 16 rows tcgen05's 128-row tile would be
-// nine tenths padding, and its operands would have to be converted through shared memory.)
+// its own ring in shared memory (cp.async, no barrier but the warp's own; 128 KB to 150 KB an
+// SM under way), converts them in registers and feeds mma.sync with the cache as the A
+// operand: S^T = K Q^T with 16 keys by 8 rows, O^T += V^T P^T with 16 dimensions by 8 rows,
+// so that 8 rows cost half of what a 16-row A operand would. The order of d inside a K step
+// and of V's rows is free, and is chosen so that a lane's operands are contiguous bytes: 32
+// of each of its two keys, 16 of each of its four values (byte pairs of two keys by PRMT).
+// P^T comes out of S^T's accumulators by movmatrix. (mma.sync: with 8 to 16 rows tcgen05's
+// 128-row tile would be nine tenths padding, and its operands would have to be converted
+// through shared memory. The other kernel takes over above kQ8MaxRows: 65,536 tokens of 8
+// heads, 24 rows a head: 59 us here, 67 there; 48 rows: 79 here, 68 there.)
 //
-// A chunk's 128-key blocks go round the CTA's 8 warps in steps of 16 keys; the warps'
-// (m, l, O) are merged in shared memory at the end and leave as the chunk's partial.
+// A chunk's keys go round the CTA's warps in steps of 16; the warps' (m, l, O) are merged in
+// shared memory at the end and leave as the chunk's partial, which combine.cu joins.
+//
+// Measured, both launches of the call together (B200, copy rate 6.5 TB/s): 8 sequences of
+// 32k tokens, 4 heads, 8 rows a head: 57 us, 4.7 TB/s; one sequence of 64k tokens: 25 us for
+// 67 MB, of which the loop over keys takes 13 (5.2 TB/s) and launch, the first loads' chain
+// (lengths, page table, cache), the merge and the combine the rest.
 #include "q8_device.cuh"
 #include "sm100.cuh"
 
@@ -67,8 +73,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// (The hint brings a whole key of two neighbouring heads: 57.7 -> 56.7 us for 8 sequences of
+// 32k tokens against 128 bytes, which is what no hint gives as well.)
 __device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t to, const float* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
@@ -125,7 +133,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), ctas_of(NT)) q8_rows_kernel
   constexpr int kVB = D / 8;         // value bytes of a lane
   constexpr int kPad = D + 4;
   using Rg = Ring<D, NT>;
-static_assert(ctas_of(NT) * (smem_bytes<D, NT>() + 8192) <= 228 * 1024, "shared memory");
+  static_assert(ctas_of(NT) * (smem_bytes<D, NT>() + 8192) <= 228 * 1024, "shared memory");
   static_assert(R * kPad * 4 <= Rg::kBytes, "a warp's O takes its ring's place");
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' rings
   __shared__ float sm[kWarps + kTreeSteps][R], sl[kWarps + kTreeSteps][R];  // the warps', then the tree's
@@ -386,14 +394,12 @@ static_assert(ctas_of(NT) * (smem_bytes<D, NT>() + 8192) <= 228 * 1024, "shared 
         f.v[j][1] = x.y;
       }
     }
-    {
-      if (edge) {  // rows past the sequence hold anything: no NaN into the product
+    if (edge) {  // rows past the sequence hold anything: no NaN into the product
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (k0 + 2 * c4 + (j & 1) + 8 * (j >> 1) >= c.key_end)
+      for (int j = 0; j < 4; ++j)
+        if (k0 + 2 * c4 + (j & 1) + 8 * (j >> 1) >= c.key_end)
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) f.v[j][w] = 0u;
-      }
+          for (int w = 0; w < D / 32; ++w) f.v[j][w] = 0u;
     }
     uint32_t b[NT][2];
     weigh(s, rv, b);
