@@ -140,6 +140,30 @@ def test_min_p_that_ends_before_the_other_filters():
         _check(*_sample(x, r.random(40), dtype, min_p=r.uniform(0.3, 1.0, 40), top_k=np.full(40, 500)))
 
 
+@pytest.mark.parametrize("small", [1e-6, 0.0, 2.0 ** -11])
+@pytest.mark.parametrize("few", [3, 1000])
+def test_top_k_that_ends_below_zero_with_tiny_logits_above(small, few):
+    """top-p's border lies among the large values, and hangs on what top-k left of the low ones."""
+    r = np.random.default_rng(few)
+    x = np.concatenate([np.full(2000, 1.0), np.full(few, small), np.full(3000, -1.0)])
+    rows = np.stack([r.permutation(x) for _ in range(40)])
+    p = np.linspace(0.5, 0.82, 40)
+    for dtype in ("f32", "bf16"):
+        _check(*_sample(rows, r.random(40), dtype, top_k=np.full(40, 2000 + few + 500), top_p=p))
+
+
+@pytest.mark.parametrize("scale", [0.1, 3.0, 12.0, 40.0])
+def test_logits_inside_and_outside_the_plain_bins(scale):
+    """bf16 logits below and above 32 in magnitude, and runs of small ones."""
+    r = np.random.default_rng(int(scale * 10))
+    x = r.standard_normal((24, 30000)) * scale
+    x[::3, :400] *= 1e-4
+    x[1::3, 0] = 32.0
+    x[2::3, 5] = -32.0
+    opts = dict(temperature=r.choice([0.3, 1.0, 5.0], 24), top_k=r.choice([0, 20, 3000], 24), top_p=r.choice([0.5, 0.95, 1.0], 24))
+    _check(*_sample(x, r.random(24), "bf16", **opts))
+
+
 def _step(state, call, cache, parts, gate):
     """One decoding step: attention with the new token, its logits, its choice, its append."""
     from tree_verification_attention_longspec_b200 import sample

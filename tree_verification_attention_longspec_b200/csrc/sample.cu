@@ -36,9 +36,9 @@
 // The row is read once from HBM, but HBM does not bound it: a cluster's life is a chain of
 // phases (load, largest, histogram, its sums, borders, weights, decision, find), each behind
 // a cluster barrier, with one shared-memory atomic an entry in the histogram and up to 10
-// fp64 instructions an entry in the weights. Measured (B200): 256 rows of 128,256 bf16 113
-// us (0.6 TB/s; the list's way took 238), 64 rows of 152,064 bf16 with the tree walk 35 us,
-// 534 rows of 128,256 with it 184 us, 8 rows of 32,000 fp32 22 us.
+// fp64 instructions an entry in the weights. Measured (B200): 256 rows of 128,256 bf16 109
+// us (0.6 TB/s; the list's way took 238), 64 rows of 152,064 bf16 with the tree walk 31 us,
+// 534 rows of 128,256 with it 166 us, 8 rows of 32,000 fp32 22 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -85,7 +85,12 @@ constexpr int kLut = 1024;  // e^(-b / 32) * 2^43
 constexpr int kKeys = 4096;  // bins of the histogram over bf16 values
 constexpr int kKeysPer = kKeys / kThreads;  // of a group; the cluster has a group for each thread of a CTA
 constexpr int kTable = kKeys / 2;           // weights that fit the histogram's place
+constexpr int kMags = kKeys / 2;            // magnitudes of `plain_map`: 16 octaves of 128
+constexpr int kMagEnd = 0x4200;             // their end, 32
+constexpr int kTiny = 256;                  // entries below them kept aside
 constexpr int kDataBytes = 76 * 1024;  // of the row, in shared memory
+// It arrives in pieces of two 16-byte vectors a thread.
+constexpr int kPieceVecs = 2, kPieces = (kDataBytes / 16 + kPieceVecs * kThreads - 1) / (kPieceVecs * kThreads);
 
 using u64 = unsigned long long;
 
@@ -114,7 +119,8 @@ struct Keys {
     double weight[kTable];  // later: of the bins kept
   };
   u64 mass[kThreads];  // of this CTA's groups of bins
-  uint32_t count[kThreads];
+  uint32_t n_tiny;
+  uint16_t small[kTiny];  // bits of the entries without a bin
 };
 struct Slow {
   u64 hist[kBins];          // this CTA's measure of each bin
@@ -305,11 +311,31 @@ class Sampler {
     w1_ = min(r_.n, w0_ + run_);
   }
 
+  // A CTA's shared memory lives until its peers have read it: `leave` says that this CTA has,
+  // `end` waits for the others'. (One that is done then makes room while another goes on.)
+  __device__ __forceinline__ void leave() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    left_ = true;
+  }
+  __device__ __forceinline__ void end() {
+    __syncwarp();
+    if (!left_) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+
   __device__ void run() {
     load();
     for (int i = tid_; i < kLut; i += kThreads) sh_.lut[i] = exp(-(double)i / 32.0) * (double)(1ull << kWeightBits);
-    extremes();
     const float t = a_.temperature != nullptr ? a_.temperature[row_id_] : 1.0f;
+    int k = a_.top_k != nullptr ? a_.top_k[row_id_] : 0;
+    if (k <= 0 || k >= a_.V) k = 0;
+    const float p = a_.top_p != nullptr ? a_.top_p[row_id_] : 1.0f;
+    // bf16 rows to be cut are counted while they arrive
+    const bool cuts = k > 0 || p < 1.0f, counted = !F32 && cuts && t > 0.f && a_.vec;
+    if (counted)
+      count_arriving();
+    else
+      extremes();
     if (top_ == -INFINITY) {  // nothing above -inf
       if (rank_ == 0 && tid_ == 0) a_.out[row_id_] = 0;
       return;
@@ -326,13 +352,20 @@ class Sampler {
     inv_t_ = 1.0 / (double)t;
     inv_f_ = (float)inv_t_;
     top_d_ = (double)top_;
-    int k = a_.top_k != nullptr ? a_.top_k[row_id_] : 0;
-    if (k <= 0 || k >= a_.V) k = 0;
-    const float p = a_.top_p != nullptr ? a_.top_p[row_id_] : 1.0f;
     const uint32_t least = least_key(a_.min_p != nullptr ? a_.min_p[row_id_] : 0.0f, t);
     const float u = a_.uniform[row_id_];
     if constexpr (!F32) {
-      if ((k > 0 || p < 1.0f) && resolve_keys(k, p, t, least, u)) return;
+      if (cuts) {
+        KeyMap map;
+        if (counted && plain_map(t, &map)) {
+          if (resolve_keys(map, k, p, least, u)) return;
+          cl_.sync();
+        }
+        if (key_map(t, &map)) {
+          count_all(map);
+          if (resolve_keys(map, k, p, least, u)) return;
+        }
+      }
       cl_.sync();  // the memory changes hands
     }
     if (resolve(k, p, least, u)) return;
@@ -356,6 +389,7 @@ class Sampler {
   Shared& sh_;
   cg::cluster_group cl_;
   int tid_, lane_, warp_, rank_, size_, lo_, run_, w0_, w1_;
+  bool left_ = false;  // the same in all threads
   int64_t row_id_;
   Row<F32> r_;
   float top_, low_;  // largest and smallest logit
@@ -446,9 +480,16 @@ class Sampler {
     uint8_t* to = static_cast<uint8_t*>(const_cast<void*>(r_.s));
     const uint8_t* from = static_cast<const uint8_t*>(r_.g);
     const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-    for (int v = tid_; v < n_vec; v += kThreads)
-      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(at + 16 * v), "l"(from + 16 * (int64_t)v) : "memory");
-    asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+#pragma unroll
+      for (int e = 0; e < kPieceVecs; ++e) {
+        const int v = (c * kPieceVecs + e) * kThreads + tid_;
+        if (v < n_vec)
+          asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(at + 16 * v), "l"(from + 16 * (int64_t)v) : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
     for (int i = n_vec * kPer + tid_; i < r_.cap; i += kThreads) {
       if constexpr (F32)
         reinterpret_cast<float*>(to)[i] = static_cast<const float*>(r_.g)[i];
@@ -457,28 +498,39 @@ class Sampler {
     }
   }
 
-  // The row's largest and smallest logit (NaN skipped).
-  __device__ void extremes() {
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
+  // The largest and smallest of what `take` saw; NaN skipped.
+  struct Ends {
     float mx = -INFINITY, mn = INFINITY;
-    auto take = [&](float x) {
+    uint32_t m2 = 0xff80ff80u, n2 = 0x7f807f80u;  // -inf, +inf
+    __device__ __forceinline__ void take(float x) {
       mx = fmaxf(mx, x);
       mn = fminf(mn, x);
-    };
-    if constexpr (F32) {
-      each([&](float x, uint32_t) { take(x); });
-    } else {
-      uint32_t m2 = 0xff80ff80u, n2 = 0x7f807f80u;  // -inf, +inf
-      each_words(
-          [&](const uint4& v) {
-            m2 = max_bf16x2(m2, max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w)));
-            n2 = min_bf16x2(n2, min_bf16x2(min_bf16x2(v.x, v.y), min_bf16x2(v.z, v.w)));
-          },
-          take);
+    }
+    __device__ __forceinline__ void take(const uint4& v) {  // of bf16
+      m2 = max_bf16x2(m2, max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w)));
+      n2 = min_bf16x2(n2, min_bf16x2(min_bf16x2(v.x, v.y), min_bf16x2(v.z, v.w)));
+    }
+    __device__ __forceinline__ void join() {
       mx = fmaxf(mx, fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u)));
       mn = fminf(mn, fminf(__uint_as_float(n2 << 16), __uint_as_float(n2 & 0xffff0000u)));
     }
+  };
+
+  // The row's largest and smallest logit.
+  __device__ void extremes() {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    Ends ends;
+    if constexpr (F32)
+      each([&](float x, uint32_t) { ends.take(x); });
+    else
+      each_words([&](const uint4& v) { ends.take(v); }, [&](float x) { ends.take(x); });
+    share_ends(ends);
+  }
+  // top_ and low_ from the threads' ends; a barrier of the cluster.
+  __device__ void share_ends(Ends& ends) {
+    if constexpr (!F32) ends.join();
+    float mx = ends.mx, mn = ends.mn;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -880,10 +932,17 @@ class Sampler {
   // [top - 31 t, top], some 4000 of them down to 2^-13. Bins for each, in falling order, make
   // the histogram exact: thresholds and sums come from counts times weights, without a list,
   // and what is left to do for the entries themselves is to add up the kept ones' weights by
-  // runs, from a table. Smaller magnitudes have no bin: their few entries' weights are added
-  // up one by one, which does as long as the threshold lies above 0; else `resolve` decides.
+  // runs, from a table, in the one CTA that holds the token. Smaller magnitudes have no bin:
+  // their few entries' weights are added up one by one, which does as long as the threshold
+  // lies above 0; else `resolve` decides.
+  //
+  // Bins for magnitudes from 2^-11 to 32 (`plain`) ask for no largest logit, so rows inside
+  // are counted while they arrive; others once it is known, in bins below it (`key_map`).
+  // 256 rows of 128,256, top-p 0.9, stage by stage (us): launches 10, load 10, count 29 (an
+  // shared-memory atomic an entry), sums over the cluster 10,
+  // border 9, kept weight by CTA 11, by run 12, the token 7.
   struct KeyMap {
-    int ptop, zero, neg0, least, count;  // bins: ptop - magnitude | zero | neg0 + magnitude
+    int ptop, pos, zero, neg0, least, count;  // bins: ptop - magnitude (`pos` of them) | zero | neg0 + magnitude
     __device__ __forceinline__ int bin(uint32_t u) const {  // of a bf16's bits; not in [0, count): none
       const int mag = (int)(u & 0x7fffu);
       if (mag < least) return mag == 0 ? zero : -1;
@@ -895,12 +954,99 @@ class Sampler {
       return ((int)(u & 0x7fffu) ^ ~neg) + (neg ? neg0 : ptop + 1);
     }
     __device__ __forceinline__ float value(int b) const {
-      if (b == zero) return 0.f;
-      return b < zero ? __uint_as_float((uint32_t)(ptop - b) << 16) : -__uint_as_float((uint32_t)(b - neg0) << 16);
+      if (b < pos) return __uint_as_float((uint32_t)(ptop - b) << 16);
+      return b == zero ? 0.f : -__uint_as_float((uint32_t)(b - neg0) << 16);
     }
   };
+  // Bins that do not depend on the row: magnitudes from 2^-11 to 32. Smaller ones, 0 too, have none.
+  __device__ __forceinline__ static KeyMap plain() {
+    return KeyMap{kMagEnd - 1, kMags, -1, 2 * kMags - kMagEnd, kMagEnd - kMags, kKeys};
+  }
+  // Counts the row in them while it arrives, each thread the vectors that it copies itself, and
+  // finds its ends.
+  __device__ void count_arriving() {
+    const KeyMap map = plain();
+    uint32_t* hist = sh_.k.hist;
+    for (int i = tid_; i < kKeys / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid_ == 0) {
+      sh_.k.n_tiny = 0u;
+      sh_.tiny = 0ull;
+    }
+    __syncthreads();
+    Ends ends;
+    auto count = [&](uint32_t bits) {
+      const int b = map.bin(bits);
+      if ((uint32_t)b < (uint32_t)kKeys) {
+        atomicAdd(&hist[b], 1u);
+      } else if (b == -1) {
+        const uint32_t at = atomicAdd(&sh_.k.n_tiny, 1u);
+        if (at < kTiny) sh_.k.small[at] = (uint16_t)bits;
+      }
+    };
+    const int n_vec = r_.cap / kPer;
+    auto piece = [&](int c) {
+#pragma unroll
+      for (int e = 0; e < kPieceVecs; ++e) {
+        const int i = (c * kPieceVecs + e) * kThreads + tid_;
+        if (i >= n_vec) break;
+        const uint4 v = r_.words(i * kPer);
+        ends.take(v);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t small = 0x7fff7fffu;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) small = __vminu2(small, w[q] & 0x7fff7fffu);
+        if (min(small & 0xffffu, small >> 16) < (uint32_t)map.least) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            count(w[q] & 0xffffu);
+            count(w[q] >> 16);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int a = map.large_bin(w[q] & 0xffffu), b = map.large_bin(w[q] >> 16);
+            if ((uint32_t)a < (uint32_t)kKeys) atomicAdd(&hist[a], 1u);
+            if ((uint32_t)b < (uint32_t)kKeys) atomicAdd(&hist[b], 1u);
+          }
+        }
+      }
+    };
+    static_assert(kPieces == 5, "the waits below");
+    asm volatile("cp.async.wait_group 4;" ::: "memory");
+    piece(0);
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+    piece(1);
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    piece(2);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    piece(3);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    piece(4);
+    for (int i = n_vec * kPer + tid_; i < r_.n; i += kThreads) {  // the share's end, and what has no room
+      const float x = r_.load(i);
+      ends.take(x);
+      count(__float_as_uint(x) >> 16);
+    }
+    share_ends(ends);
+  }
+  // `plain`, where it holds what weighs anything in this row (whose histogram is there).
+  __device__ bool plain_map(float t, KeyMap* k) {
+    if (!(inv_f_ > 0.f && inv_f_ < INFINITY)) return false;
+    const float end = __uint_as_float((uint32_t)kMagEnd << 16);
+    bool fits = true;
+    for (int c = 0; c < size_; ++c) fits &= cl_.map_shared_rank(&sh_, c)->k.n_tiny <= kTiny;
+    if (!fits || !(top_ < end) || !(low_ > -end || top_ - kMaxX * t > -end)) return false;
+    *k = plain();
+    const uint32_t n = sh_.k.n_tiny;
+    for (uint32_t j = tid_; j < n; j += kThreads) {
+      const u64 w = weight(__uint_as_float((uint32_t)sh_.k.small[j] << 16));
+      if (w) atomicAdd(&sh_.tiny, w);
+    }
+    return true;
+  }
   // The map for this row; false where its range of values has no room.
   __device__ bool key_map(float t, KeyMap* k) const {
+    if (!(inv_f_ > 0.f && inv_f_ < INFINITY)) return false;
     const float low = top_ - kMaxX * t;  // below it, weights are 0
     if (!(low < top_) || top_ == INFINITY) return false;
     const int last = low < 0.f ? (int)min(__float_as_uint(-low) >> 16, 0x7f7eu) + 1 : 0;  // largest magnitude below 0
@@ -910,20 +1056,19 @@ class Sampler {
       const int least = max(1, last > 0 ? (p + last + 4 - kKeys) / 2 : p + 2 - kKeys);
       if (least > p) return false;
       const int zero = p - least + 1;
-      *k = KeyMap{p, zero, zero + 1 - least, least, last >= least ? zero + 2 - least + last : zero + 1};
+      *k = KeyMap{p, zero, zero, zero + 1 - least, least, last >= least ? zero + 2 - least + last : zero + 1};
     } else if (top_ == 0.f) {
       const int least = max(1, last + 2 - kKeys);
-      *k = KeyMap{-1, 0, 1 - least, least, last >= least ? 2 - least + last : 1};
+      *k = KeyMap{-1, 0, 0, 1 - least, least, last >= least ? 2 - least + last : 1};
     } else {
       const int p = (int)(__float_as_uint(-top_) >> 16);
-      *k = KeyMap{-1, -1, -p, p, last - p + 1};
+      *k = KeyMap{-1, 0, -1, -p, p, last - p + 1};
     }
     return k->count <= kKeys && k->count > 0;
   }
 
-  __device__ bool resolve_keys(int k, float p, float t, uint32_t least, float u) {
-    KeyMap map;
-    if (!(inv_f_ > 0.f && inv_f_ < INFINITY) || !key_map(t, &map)) return false;
+  // Counts the row in the map's bins.
+  __device__ void count_all(const KeyMap& map) {
     uint32_t* hist = sh_.k.hist;
     for (int i = tid_; i < kKeys / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid_ == 0) sh_.tiny = 0ull;
@@ -960,13 +1105,24 @@ class Sampler {
         [&](float x) { count(__float_as_uint(x) >> 16); });
     if (tiny) atomicAdd(&sh_.tiny, tiny);
     cl_.sync();
+  }
+
+  // The row's token from the CTAs' counts; false where they do not tell. The sums over the
+  // cluster decide the border; every CTA's own counts then give its kept weight, and only the
+  // one that the target falls in goes through its entries again.
+  __device__ bool resolve_keys(const KeyMap& map, int k, float p, uint32_t least, float u) {
+    uint4* hist = reinterpret_cast<uint4*>(sh_.k.hist);
+    const int share = kKeys / 4 / size_, in_share = rank_ * share + tid_;  // groups of four bins
+    static_assert(kKeys / 4 / 2 <= kThreads, "a thread adds up four bins");
+    uint4 own = make_uint4(0u, 0u, 0u, 0u);  // this CTA's counts where the sums take their place
+    if (tid_ < 2) sh_.tot[tid_] = 0ull;
     if (size_ > 1) {
-      const int share = kKeys / 4 / size_;
-      for (int i = rank_ * share + tid_; i < (rank_ + 1) * share; i += kThreads) {
+      if (tid_ < share) {
         uint4 v[kMaxCluster];
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r)
-          if (r < size_) v[r] = reinterpret_cast<const uint4*>(cl_.map_shared_rank(&sh_, r)->k.hist)[i];
+          if (r < size_) v[r] = reinterpret_cast<const uint4*>(cl_.map_shared_rank(&sh_, r)->k.hist)[in_share];
+        own = hist[in_share];
 #pragma unroll
         for (int r = 1; r < kMaxCluster; ++r)
           if (r < size_) {
@@ -975,40 +1131,83 @@ class Sampler {
             v[0].z += v[r].z;
             v[0].w += v[r].w;
           }
-        reinterpret_cast<uint4*>(hist)[i] = v[0];
+        hist[in_share] = v[0];
       }
       __syncthreads();
     }
-    {  // its groups' counts and weights, size_ threads a group
+    {  // its groups' weights, size_ threads a group
       const int g = tid_ / size_, b0 = (rank_ * (kThreads / size_) + g) * kKeysPer;
       u64 mass = 0;
-      uint32_t cnt = 0;
       for (int e = tid_ % size_; e < kKeysPer; e += size_) {
-        const uint32_t c = hist[b0 + e];
-        cnt += c;
+        const uint32_t c = sh_.k.hist[b0 + e];
         if (c) mass += c * weight(map.value(b0 + e));
       }
-      for (int o = size_ / 2; o > 0; o /= 2) {
-        cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-        mass += __shfl_xor_sync(0xffffffffu, mass, o);
-      }
-      if (tid_ % size_ == 0) {
-        sh_.k.mass[g] = mass;
-        sh_.k.count[g] = cnt;
-      }
+      for (int o = size_ / 2; o > 0; o /= 2) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+      if (tid_ % size_ == 0) sh_.k.mass[g] = mass;
     }
     cl_.sync();
     if (rank_ == 0) look_keys(map, (uint32_t)k, p, least, u);
     cl_.sync();
     const KeyVerdict o = cl_.map_shared_rank(&sh_, 0)->keys;
     if (!o.ok) return false;
-    // weights of the bins kept whole, where the histogram was
-    const int whole = (int)o.bin;
-    const float least_f = least > 0u ? of_key(least) : -INFINITY;
-    for (int b = tid_; b < min(whole, kTable); b += kThreads) sh_.k.weight[b] = (double)weight(map.value(b));
-    __syncthreads();
-    const float edge = o.edge;
+    const int whole = (int)o.bin;  // bins kept whole
+    const float least_f = least > 0u ? of_key(least) : -INFINITY, edge = o.edge;
     const uint32_t cut = edge >= least_f ? o.m : 0u;  // of the edge's own entries, the first `cut` are kept
+    {  // this CTA's kept weight but for the edge's entries, and their number
+      u64 keep = 0;
+      auto four = [&](uint4 v, int b) {
+#pragma unroll 1  // (code that runs once costs its fetching)
+        for (int e = 0; e < 4; ++e, ++b) {
+          if (v.x && b < whole && map.value(b) >= least_f) keep += v.x * weight(map.value(b));
+          if (b == whole) sh_.tot[1] = v.x;
+          v = make_uint4(v.y, v.z, v.w, 0u);
+        }
+      };
+#pragma unroll 1
+      for (int i = tid_; i < kKeys / 4 + kThreads; i += kThreads) {
+        const bool rest = i >= kKeys / 4;  // at last, the counts that the sums replaced
+        const int at = rest ? in_share : i;
+        if ((rest ? size_ > 1 && tid_ < share : size_ == 1 || i / share != rank_) && 4 * at <= whole)
+          four(rest ? own : hist[at], 4 * at);
+      }
+      if (__any_sync(0xffffffffu, keep != 0ull)) {
+        keep = warp_sum64(keep);
+        if (lane_ == 0) atomicAdd(&sh_.tot[0], keep);
+      }
+    }
+    cl_.sync();
+    // the CTA, the warp's run, and the part of it that the target falls in; `pre`: kept weight
+    // before it, `seen`: the edge's entries before it
+    auto kept_of = [&](u64 whole_w, uint32_t n, uint32_t seen) {
+      return whole_w + (u64)(min(seen + n, cut) - min(seen, cut)) * o.w;
+    };
+    u64 pre = 0, cta_w[kMaxCluster];
+    uint32_t seen = 0, cta_n[kMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (c < size_) {
+        const Shared* q = cl_.map_shared_rank(&sh_, c);
+        cta_w[c] = q->tot[0];
+        cta_n[c] = (uint32_t)q->tot[1];
+      }
+    leave();
+    int owner = -1;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (c < size_ && owner < 0) {
+        const u64 mine = kept_of(cta_w[c], cta_n[c], seen);
+        if (o.target < pre + mine) {
+          owner = c;
+        } else {
+          pre += mine;
+          seen += cta_n[c];
+        }
+      }
+    if (owner != rank_) return true;
+    // weights of the bins kept whole, where the histogram was
+    const int from = top_ > 0.f ? map.ptop - (int)(__float_as_uint(top_) >> 16) : map.pos;  // bins above hold nothing
+    for (int b = from + tid_; b < min(whole, kTable); b += kThreads) sh_.k.weight[b] = (double)weight(map.value(b));
+    __syncthreads();
     auto weight_at = [&](float x) {
       const int b = map.bin(__float_as_uint(x) >> 16);
       return b < kTable ? sh_.k.weight[b] : (double)weight(x);
@@ -1048,172 +1247,172 @@ class Sampler {
     equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane_ == 0) {
       sh_.ws[0][warp_] = s_keep;
-      sh_.ws[1][warp_] = equal;
+      sh_.cwarp[warp_] = equal;
     }
     __syncthreads();
-    if (warp_ < 2) {
-      const u64 v = warp_sum64(lane_ < kWarps ? sh_.ws[warp_][lane_] : 0ull);
-      if (lane_ == 0) sh_.tot[warp_] = v;
-    }
-    cl_.sync();
-    // the CTA, the warp's run, and the part of it that the target falls in; `pre`: kept weight
-    // before it, `seen`: the edge's entries before it
-    auto kept_of = [&](u64 whole_w, u64 n, u64 seen) { return whole_w + (min(seen + n, (u64)cut) - min(seen, (u64)cut)) * o.w; };
-    u64 pre = 0, seen = 0;
-    int owner = -1;
-#pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) {
-      if (c >= size_ || owner >= 0) continue;
-      const Shared* q = cl_.map_shared_rank(&sh_, c);
-      const u64 n = q->tot[1], mine = kept_of(q->tot[0], n, seen);
-      if (o.target < pre + mine) {
-        owner = c;
-      } else {
-        pre += mine;
-        seen += n;
-      }
-    }
-    if (owner != rank_) return true;
-    int w = 0;
-    for (; w < kWarps - 1; ++w) {
-      const u64 mine = kept_of(sh_.ws[0][w], sh_.ws[1][w], seen);
-      if (o.target < pre + mine) break;
-      pre += mine;
-      seen += sh_.ws[1][w];
-    }
+    // Of 32 parts in order, a lane's own weighing `w` and holding `n` of the edge's entries: the
+    // kept weight and the edge's entries before it, and whether the target falls in it.
+    auto place = [&](u64 w, uint32_t n, u64* before, uint32_t* same) {
+      *same = seen + warp_scan(n, lane_) - n;
+      const u64 mine = kept_of(w, n, *same);
+      *before = pre + warp_scan(mine, lane_) - mine;
+      return o.target >= *before && o.target < *before + mine;
+    };
+    u64 at;
+    uint32_t same;
+    const bool is_run = place(lane_ < kWarps ? sh_.ws[0][lane_] : 0ull, lane_ < kWarps ? sh_.cwarp[lane_] : 0u, &at, &same);
+    const int w = __ffs(__ballot_sync(0xffffffffu, is_run)) - 1;
+    if (w < 0) return true;  // not reached: the runs' sums are the CTA's
+    pre = __shfl_sync(0xffffffffu, at, w);
+    seen = __shfl_sync(0xffffffffu, same, w);
+    // that run again, a part for each warp and of that for each lane
     const int r0 = min(r_.n, w * run_), r1 = min(r_.n, r0 + run_);
-    const int sub = (run_ / 64 + kWarps - 1) / kWarps * 64;
-    const int i0 = min(r1, r0 + warp_ * sub), i1 = min(r1, i0 + sub);
+    const int per = (run_ + kThreads - 1) / kThreads;
+    const int i0 = min(r1, r0 + tid_ * per), i1 = min(r1, i0 + per);
     auto whole_weight = [&](float x) { return x > edge && x >= least_f ? (u64)weight_at(x) : 0ull; };
     u64 s = 0;
     uint32_t n = 0;
-    for (int i = i0 + lane_; i < i1; i += 32) {
+    for (int i = i0; i < i1; ++i) {
       const float x = r_.one(i);
       s += whole_weight(x);
       n += x == edge ? 1u : 0u;
     }
-    s = warp_sum64(s);
-    n = __reduce_add_sync(0xffffffffu, n);
+    const u64 warp_s = warp_sum64(s);
+    const uint32_t warp_n = __reduce_add_sync(0xffffffffu, n);
     if (lane_ == 0) {
-      sh_.scan[warp_] = s;
-      sh_.cwarp[warp_] = n;
+      sh_.scan[warp_] = warp_s;
+      sh_.cpart[0][warp_] = warp_n;
     }
     __syncthreads();
-    for (int q = 0; q < warp_; ++q) {
-      pre += kept_of(sh_.scan[q], sh_.cwarp[q], seen);
-      seen += sh_.cwarp[q];
-    }
-    if (o.target < pre || o.target >= pre + kept_of(s, n, seen)) return true;
-    for (int i = i0; i < i1; i += 32) {
-      const float x = i + lane_ < i1 ? r_.one(i + lane_) : __uint_as_float(0x7fffffffu);
-      const uint32_t same = __ballot_sync(0xffffffffu, x == edge);
-      const u64 at = seen + __popc(same & ((1u << lane_) - 1u));
-      const u64 mine = x == edge ? (at < cut ? o.w : 0ull) : whole_weight(x);
-      const u64 upto = pre + warp_scan(mine, lane_);
-      if (o.target < upto && o.target >= upto - mine) a_.out[row_id_] = lo_ + i + lane_;
-      pre = __shfl_sync(0xffffffffu, upto, 31);
-      if (o.target < pre) break;
-      seen += __popc(same);
+    place(lane_ < kWarps ? sh_.scan[lane_] : 0ull, lane_ < kWarps ? sh_.cpart[0][lane_] : 0u, &at, &same);
+    pre = __shfl_sync(0xffffffffu, at, warp_);
+    seen = __shfl_sync(0xffffffffu, same, warp_);
+    if (place(s, n, &at, &same)) {
+      for (int i = i0; i < i1; ++i) {
+        const float x = r_.one(i);
+        u64 mine = whole_weight(x);
+        if (x == edge) mine = same++ < cut ? o.w : 0ull;
+        if (o.target >= at && o.target < at + mine) a_.out[row_id_] = lo_ + i;
+        at += mine;
+      }
     }
     return true;
   }
 
-  // Rank 0: the summed histogram's verdict, into its sh_.keys. Thread t has group t.
+  // Rank 0: the summed histogram's verdict, into its sh_.keys. Thread t has group t. The group
+  // that holds a border is looked through by eight lanes, a bin each: every other CTA of the
+  // cluster waits for this one.
   __device__ void look_keys(const KeyMap& map, uint32_t k, float p, uint32_t least, float u) {
-    const int groups = kThreads / size_, b0 = kKeysPer * tid_;  // of a CTA; the group's first bin
+    const int groups = kThreads / size_;  // of a CTA
     const Shared* o = cl_.map_shared_rank(&sh_, tid_ / groups);
-    const uint32_t own = o->k.count[tid_ % groups];
-    u64 mass = o->k.mass[tid_ % groups];
-    u64 tiny = 0;
+    u64 mass = o->k.mass[tid_ % groups], tiny = 0;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
       if (r < size_) tiny += cl_.map_shared_rank(&sh_, r)->tiny;
-    auto count_of = [&](int e) { return o->k.hist[b0 + e]; };
+    // of group g, lane e's bin: its entries, and (none where there are none) their weight
+    auto count_of = [&](int g) {
+      return lane_ < kKeysPer ? cl_.map_shared_rank(&sh_, g / groups)->k.hist[kKeysPer * g + lane_] : 0u;
+    };
     // top-k's border: bins before bk are kept whole, `room` entries of it
     int bk = kKeys;  // none: the entries with a bin are fewer
     uint32_t room = 0;
+    if (tid_ == 0) sh_.bins[0] = sh_.bins[1] = kThreads;  // the borders' groups
     if (k > 0) {
+      uint32_t own = 0;
+#pragma unroll
+      for (int e = 0; e < kKeysPer / 4; ++e) {
+        const uint4 v = reinterpret_cast<const uint4*>(o->k.hist)[tid_ * (kKeysPer / 4) + e];
+        own += v.x + v.y + v.z + v.w;
+      }
       const uint32_t inc = warp_scan(own, lane_);
       if (lane_ == 31) sh_.cwarp[warp_] = inc;
-      if (tid_ == 0) sh_.bin = kKeys;
       __syncthreads();
-      uint32_t before = inc - own;
-      for (int w = 0; w < warp_; ++w) before += sh_.cwarp[w];
-      if (k > before && k <= before + own) {  // this thread's group has it
-        int e = 0;
-        mass = 0;
-        for (;; ++e) {
-          const uint32_t c = count_of(e);
-          if (before + c >= k) break;
-          before += c;
-          if (c) mass += c * weight(map.value(b0 + e));
-        }
-        mass += (k - before) * weight(map.value(b0 + e));
-        sh_.bin = (uint32_t)(b0 + e);
+      const uint32_t warps = lane_ < warp_ ? sh_.cwarp[lane_] : 0u;
+      const uint32_t before = __reduce_add_sync(0xffffffffu, warps) + inc - own;
+      if (k > before && k <= before + own) {
+        sh_.bins[0] = (uint32_t)tid_;
         sh_.cut = k - before;
       }
       __syncthreads();
-      bk = (int)sh_.bin;
-      room = sh_.cut;
-      if (b0 > bk) mass = 0;
+      const int g = (int)sh_.bins[0];
+      if (g < kThreads) {
+        const uint32_t c = count_of(g), upto = warp_scan(c, lane_), left = sh_.cut;  // of the group
+        const int e = __ffs(__ballot_sync(0xffffffffu, upto >= left)) - 1;
+        bk = kKeysPer * g + e;
+        room = left - __shfl_sync(0xffffffffu, upto - c, e);
+        if (warp_ == g / 32) {  // its weight is what is kept of it
+          const uint32_t kept = lane_ < e ? c : lane_ == e ? room : 0u;
+          const u64 w = warp_sum64(kept ? kept * weight(map.value(kKeysPer * g + lane_)) : 0ull);
+          if (tid_ == g) mass = w;
+        }
+        if (tid_ > g) mass = 0;
+      }
+      if (bk < map.pos) tiny = 0;  // top-k ends above them
+    } else {
+      __syncthreads();
     }
-    if (bk < map.zero) tiny = 0;  // top-k ends above them
     const u64 minc = warp_scan(mass, lane_);
     if (lane_ == 31) sh_.scan[warp_] = minc;
-    if (tid_ == 0) sh_.keys.ok = 0;
     __syncthreads();
-    u64 mbefore = minc - mass, all = tiny;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp_) mbefore += sh_.scan[w];
-      all += sh_.scan[w];
-    }
+    const u64 sums = lane_ < kWarps ? sh_.scan[lane_] : 0ull, upto = warp_scan(sums, lane_);
+    const u64 all = __shfl_sync(0xffffffffu, upto, kWarps - 1) + tiny;
+    const u64 before = __shfl_sync(0xffffffffu, upto - sums, warp_) + minc - mass;
     u64 goal = all;  // the border holds the goal-th unit of weight: the last kept
     if (p < 1.0f) {
       const double g = ceil((double)p * (double)all);
       goal = g >= 1.0 ? min((u64)g, all) : 1ull;
     }
-    if (goal > mbefore && goal <= mbefore + mass) {
-      u64 at = mbefore;
-      for (int e = 0; e < kKeysPer; ++e) {
-        const int b = b0 + e;
-        const uint32_t c = b < bk ? count_of(e) : b == bk ? room : 0u;
-        const u64 w = c ? weight(map.value(b)) : 0ull;
-        if (at + c * w < goal) {
-          at += c * w;
-          continue;
-        }
-        sh_.keys.edge = map.value(b);
-        sh_.keys.bin = (uint32_t)b;
-        sh_.keys.w = w;
-        sh_.keys.m = (uint32_t)((goal - at + w - 1) / w);
-        sh_.total = at + (u64)sh_.keys.m * w;  // kept, but for min-p
-        // entries without a bin lie among those of the zero: they do not matter above it
-        sh_.keys.ok = tiny == 0ull || b < map.zero ? 1 : 0;
-        break;
-      }
+    if (goal > before && goal <= before + mass) {
+      sh_.bins[1] = (uint32_t)tid_;
+      sh_.above = before;
     }
     __syncthreads();
-    if (!sh_.keys.ok) return;
-    u64 z = sh_.total;
-    const float least_f = least > 0u ? of_key(least) : -INFINITY;
-    if (sh_.keys.edge < least_f) {  // min-p ends before the border
-      u64 kept = 0;
-      if (map.value(b0) >= least_f) {
-        if (map.value(b0 + kKeysPer - 1) >= least_f)
-          kept = mass;
-        else
-          for (int e = 0; e < kKeysPer && map.value(b0 + e) >= least_f; ++e) {
-            const uint32_t c = count_of(e);
-            if (c) kept += c * weight(map.value(b0 + e));
-          }
-      }
-      kept = warp_sum64(kept);
-      if (lane_ == 0) sh_.wsum[warp_] = kept;
-      __syncthreads();
-      z = 0;
-      for (int w = 0; w < kWarps; ++w) z += sh_.wsum[w];
+    const int g = (int)sh_.bins[1];
+    if (g == kThreads) {  // among the entries without a bin
+      if (tid_ == 0) sh_.keys.ok = 0;
+      return;
     }
-    if (tid_ == 0) sh_.keys.target = target_of(u, z);
+    const int b = kKeysPer * g + lane_;
+    if (warp_ == 0) {
+      uint32_t c = count_of(g);
+      if (b >= bk) c = b == bk ? room : 0u;
+      const u64 w = c ? weight(map.value(b)) : 0ull, at = sh_.above + warp_scan(c * w, lane_) - c * w;
+      if (at < goal && goal <= at + c * w) {
+        uint32_t m = (uint32_t)((float)(goal - at) / (float)w);  // off by less than one: at most 2^20
+        while (m * w < goal - at) ++m;
+        while (m > 1u && (m - 1u) * w >= goal - at) --m;
+        const u64 z = at + m * w;  // kept, but for min-p
+        // entries without a bin lie among those of the zero: they matter neither to a border
+        // above it nor, where top-k ends above them too, to its sums
+        const int ok = tiny == 0ull || (b < map.pos && k == 0) ? 1 : 0;
+        sh_.keys = KeyVerdict{target_of(u, z), w, map.value(b), m, (uint32_t)b, ok};
+      }
+    }
+    if (least == 0u) return;
+    __syncthreads();
+    const float least_f = of_key(least);
+    if (!sh_.keys.ok || sh_.keys.edge >= least_f) return;
+    // min-p ends before the border: the bins down to it, of the groups before the border's whole
+    u64 kept = 0;
+    if (tid_ <= g && map.value(kKeysPer * tid_) >= least_f) {
+      if (tid_ < g && map.value(kKeysPer * tid_ + kKeysPer - 1) >= least_f) {
+        kept = mass;
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < kKeysPer; ++e) {
+          const float x = map.value(kKeysPer * tid_ + e);
+          const uint32_t c = x >= least_f ? o->k.hist[kKeysPer * tid_ + e] : 0u;
+          if (c) kept += c * weight(x);
+        }
+      }
+    }
+    kept = warp_sum64(kept);
+    if (lane_ == 0) sh_.wsum[warp_] = kept;
+    __syncthreads();
+    if (warp_ == 0) {
+      const u64 z = warp_sum64(lane_ < kWarps ? sh_.wsum[lane_] : 0ull);
+      if (lane_ == 0) sh_.keys.target = target_of(u, z);
+    }
   }
 
   // The row's token, by way of the list; false where the list does not hold the border (then
@@ -1339,6 +1538,7 @@ class Sampler {
         pre += tot[c];
       }
     }
+    leave();
     if (o.owner != rank_) return true;
     if (any) {
       // the list's kept weights by run of this CTA
@@ -1539,8 +1739,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   {
     Sampler<F32> s(a, sh, smem);
     s.run();
+    s.end();
   }
-  cg::this_cluster().sync();  // a CTA's shared memory lives until its peers have read it
 }
 
 struct WalkArgs {
