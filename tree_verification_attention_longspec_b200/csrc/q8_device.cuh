@@ -111,6 +111,7 @@ struct AppendArgs {
   int32_t B, Hkv, d, T;
   int32_t rows;     // rows of k_new / v_new
   int32_t max_new;  // rows a sequence may append
+  int32_t team_shift;  // log2 of the warps of a block (the kernel's own)
   int64_t blocks;   // scale blocks that the sequences may touch in all
 };
 

@@ -938,9 +938,9 @@ class Sampler {
   //
   // Bins for magnitudes from 2^-11 to 32 (`plain`) ask for no largest logit, so rows inside
   // are counted while they arrive; others once it is known, in bins below it (`key_map`).
-  // 256 rows of 128,256, top-p 0.9, stage by stage (us): launches 10, load 10, count 29 (an
-  // shared-memory atomic an entry), sums over the cluster 10,
-  // border 9, kept weight by CTA 11, by run 12, the token 7.
+  // 256 rows of 128,256, top-p 0.9, stage by stage (us): launches 10, load 10, count 29 (a
+  // shared-memory atomic an entry), sums over the cluster 10, border 9, kept weight by CTA
+  // 11, by run 12, the token 7.
   struct KeyMap {
     int ptop, pos, zero, neg0, least, count;  // bins: ptop - magnitude (`pos` of them) | zero | neg0 + magnitude
     __device__ __forceinline__ int bin(uint32_t u) const {  // of a bf16's bits; not in [0, count): none
