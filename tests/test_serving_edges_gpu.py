@@ -49,6 +49,25 @@ def test_commit_of_a_path_longer_than_its_tree_leaves_room_for_the_others():
     pool.expect({"k": rows, "v": rows}, cu, [128, 8])
 
 
+@pytest.mark.parametrize("size", [1e-3, 1.0, 300.0])
+@pytest.mark.parametrize("d,page,block", [(64, 16, 16), (64, 128, 128), (128, 128, 32), (128, 64, 64), (128, 256, 128)])
+def test_append_to_blocks_of_another_writers_scale(d, page, block, size):
+    """Scales of 1.25 * 2^k: kept where they are large enough (the rows are divided by them), and
+    else replaced. (8-bit values over 5 / 4 come no nearer to the middle of two codes, short of
+    lying on it, than 2^-12 of themselves, so the kernel's division in fp32 rounds to the same.)"""
+    r = np.random.default_rng(block)
+    lens, new = (block - 1, block // 2 + 3, 5, 0), (block + 1, 2 * block, 1, block)
+    pool = Pool(lens, [a + b for a, b in zip(lens, new)], 3, d, page, block, seed=d)
+    for w in "kv":
+        pool.scales[w] *= np.float32(1.25)
+    cache = pool.device()
+    cu_new = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    k, v = (bf16(size * r.standard_normal((sum(new), 3, d))) for _ in range(2))
+    cu = cache.append(k.cuda(), v.cuda(), pool.cu, _dev(cu_new), max(new))
+    split = [list(x) for x in np.split(f64(k), cu_new[1:-1])], [list(x) for x in np.split(f64(v), cu_new[1:-1])]
+    pool.expect({"k": split[0], "v": split[1]}, cu, [a + b for a, b in zip(lens, new)])
+
+
 def test_sequences_that_share_pages():
     """A common prompt's pages in every sequence's table."""
     case = Case((640, 640, 640), 8, 2, 128, 5, 64, 32, seed=4)
