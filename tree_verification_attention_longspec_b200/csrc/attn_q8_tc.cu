@@ -93,8 +93,9 @@ struct Bars {
   uint64_t raw_full[8], raw_empty[8];   // raw tiles
   uint64_t full[6], empty[6];           // f16 tiles
   uint64_t table_full[kTables];         // a block's scales
-  uint64_t s_full[kTiles];              // S_t(j) is in TMEM (and O_t holds every PV before it)
+  uint64_t s_full[kTiles][2];           // half h of S_t(j) is in TMEM (and O_t holds every PV but the last half's)
   uint64_t p_full[kTiles][2];           // half h of P_t(j) is in TMEM
+  uint64_t pv_done[kTiles];             // O_t holds one more half
   uint64_t o_full[kTiles];              // every MMA of tile t finished
   uint64_t tree_full;                   // tree_max is there
   uint32_t tmem_base;
@@ -124,6 +125,17 @@ constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn_major) {
          | ((b_mn_major ? 1u : 0u) << 16)          // B major-ness (A is K-major)
          | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);  // M / 16
+}
+
+// True in one lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // AND of `pred` over the `n` threads that meet at named barrier `id`.
@@ -202,49 +214,36 @@ __device__ __forceinline__ void make_p(const float (&s)[kHalf], const float* ck,
   }
 }
 
-// Tree mask (LongSpec, gist.science summary, section 2C, "Baum-Maskierung") on the
-// scores of the tree block in this thread's TMEM lane: key x (tree node x) stays visible
-// when x is the row's node or one of its ancestors, found by following parent links.
-// Every link is checked (node 0 is the root with parent -1, any other node's parent
-// lies below it), so the walk ends; a failed check raises `bad`. node < 0 (a padding
-// row) masks every key. The scores go back to TMEM as -inf where masked.
-__device__ __forceinline__ bool mask_tree_scores(const int16_t* parent, uint32_t tS, int node) {
-  uint32_t am[4] = {0u, 0u, 0u, 0u};
-  bool bad = false;
+// Tree mask (LongSpec, gist.science summary, section 2C, "Baum-Maskierung") of half h of the
+// tree block's scores x: key (tree node) y stays visible when y is the row's node or one of
+// its ancestors, found by following parent links. Every link is checked (node 0 is the root
+// with parent -1, any other node's parent lies below it), so the walk ends; false: a check
+// failed. node < 0 (a padding row) masks every key.
+__device__ __forceinline__ bool mask_tree_scores(const int16_t* parent, float (&x)[kHalf], int node, int h) {
+  uint32_t am[2] = {0u, 0u};
+  bool good = true;
   if (node >= 0) {
-    int x = node;
+    int y = node;
     for (int step = 0; step <= kMaxTree; ++step) {
-      const uint32_t bit = 1u << (x & 31);
-      const int w = x >> 5;
-      am[0] |= w == 0 ? bit : 0u;
-      am[1] |= w == 1 ? bit : 0u;
-      am[2] |= w == 2 ? bit : 0u;
-      am[3] |= w == 3 ? bit : 0u;
-      const int pp = parent[x];
-      if (x == 0) {
-        bad = pp != -1;
+      const uint32_t bit = (y >> 6) == h ? 1u << (y & 31) : 0u;
+      am[0] |= y & 32 ? 0u : bit;
+      am[1] |= y & 32 ? bit : 0u;
+      const int pp = parent[y];
+      if (y == 0) {
+        good = pp == -1;
         break;
       }
-      if (pp < 0 || pp >= x) {
-        bad = true;
+      if (pp < 0 || pp >= y) {
+        good = false;
         break;
       }
-      x = pp;
+      y = pp;
     }
   }
-  __syncwarp();  // the TMEM accesses below are warp-collective
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t r[32];
-    tmem_ld32(tS + 32 * q, r);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (!((am[q] >> e) & 1u)) r[e] = __float_as_uint(-INFINITY);
-    tmem_st32(tS + 32 * q, r);
-  }
-  tmem_wait_st();
-  return bad;
+  for (int e = 0; e < kHalf; ++e)
+    if (!((am[e >> 5] >> (e & 31)) & 1u)) x[e] = -INFINITY;
+  return good;
 }
 
 template <int D>
@@ -340,7 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     }
     for (int s = 0; s < kTables; ++s) mbar_init(&bars->table_full[s], 1);
     for (int t = 0; t < kTiles; ++t) {
-      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->s_full[t][0], 1);
+      mbar_init(&bars->s_full[t][1], 1);
+      mbar_init(&bars->pv_done[t], 1);
       mbar_init(&bars->p_full[t][0], 128);
       mbar_init(&bars->p_full[t][1], 128);
       mbar_init(&bars->o_full[t], 1);
@@ -620,136 +621,147 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     asm volatile("bar.sync 1, 288;" ::: "memory");
 
     if (warp == kMmaWarp) {
-      if (lane == 0) {
-        // -------------------------------------------------------------- MMA issuer
-        constexpr uint32_t idesc_qk = umma_idesc_f16(128, kBlockN, false);
-        constexpr uint32_t idesc_pv = umma_idesc_f16(128, D, true);
-        // A descriptor differs from another of the same kind only in its start-address
-        // field (address >> 4 in the low 14 bits; shared addresses stay below 256 KB, so
-        // adding an offset never carries out of it): build the bases once, add offsets.
-        const uint64_t dq0 = umma_sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
-        constexpr uint32_t kQPanel16 = C::kQPanelBytes >> 4, kQTile16 = (128 * 128) >> 4;
-        const uint64_t dk0 = umma_sdesc_sw128(smem_u32(smem + C::kSlotOff), 16, 1024);
-        const uint64_t dv0 = umma_sdesc_sw128(smem_u32(smem + C::kSlotOff), C::kPanelBytes, 1024);
-        constexpr uint32_t kTile16 = C::kTileBytes >> 4, kPanel16 = C::kPanelBytes >> 4;
-        // S_t = Q_t K^T into tile t's score buffer; K sits in ring slot `slot`
-        auto issue_qk = [&](int t, int slot) {
-          const uint64_t dq = dq0 + (uint64_t)((alt ? 0 : t) * kQTile16);  // both tiles read tile 0's Q rows when alternating
-          const uint64_t dk = dk0 + (uint64_t)(slot * kTile16);
-          const uint32_t tS = tbase + C::kColS + t * kBlockN;
+      // ---------------------------------------------------------------- MMA issuer
+      // The whole warp goes along and one lane issues, so that what an MMA is given (the same in
+      // all lanes) stays in uniform registers: moved there from one lane's, each took 60 cycles.
+      const bool lead = elect_one();
+      const uint32_t tb = __reduce_max_sync(0xffffffffu, tbase);
+      const int blocks = (int)__reduce_max_sync(0xffffffffu, (uint32_t)nbt);
+      const bool by_turns = __any_sync(0xffffffffu, alt);
+      constexpr uint32_t idesc_qk = umma_idesc_f16(128, kHalf, false);
+      constexpr uint32_t idesc_pv = umma_idesc_f16(128, D, true);
+      // A descriptor differs from another of the same kind only in its start-address
+      // field (address >> 4 in the low 14 bits; shared addresses stay below 256 KB, so
+      // adding an offset never carries out of it): build the bases once, add offsets.
+      const uint64_t dq0 = umma_sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
+      constexpr uint32_t kQPanel16 = C::kQPanelBytes >> 4, kQTile16 = (128 * 128) >> 4;
+      const uint64_t dk0 = umma_sdesc_sw128(smem_u32(smem + C::kSlotOff), 16, 1024);
+      const uint64_t dv0 = umma_sdesc_sw128(smem_u32(smem + C::kSlotOff), C::kPanelBytes, 1024);
+      constexpr uint32_t kTile16 = C::kTileBytes >> 4, kPanel16 = C::kPanelBytes >> 4;
+      auto commit = [&](uint64_t* bar) {
+        if (lead) umma_commit(bar);
+      };
+      // half h of S_t = Q_t K^T into that half of tile t's score buffer; K sits in ring slot `slot`
+      auto issue_qk = [&](int t, int slot, int h) {
+        const uint64_t dq = dq0 + (uint64_t)((by_turns ? 0 : t) * kQTile16);  // both tiles read tile 0's Q rows by turns
+        const uint64_t dk = dk0 + (uint64_t)(slot * kTile16 + h * ((kHalf * 128) >> 4));
+        const uint32_t tS = tb + C::kColS + t * kBlockN + h * kHalf;
+        if (lead) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t koff = (kk & 3) * 2;  // 32 bytes per K step inside a panel (16-byte units)
             umma_ss(tS, dq + (kk >> 2) * kQPanel16 + koff, dk + (kk >> 2) * kPanel16 + koff, idesc_qk,
                     kk > 0 ? 1u : 0u);
           }
-          umma_commit(&bars->s_full[t]);
-        };
-        // O_t += P_t V over keys [64h, 64h+64) of block j: four K = 16 steps, P from TMEM
-        auto issue_pv = [&](int t, int slot, int j, int h) {
-          const uint64_t dv = dv0 + (uint64_t)(slot * kTile16);
-          const uint32_t tP = tbase + C::kColS + t * kBlockN;
-          const uint32_t tO = tbase + C::kColO + t * D;
+          umma_commit(&bars->s_full[t][h]);
+        }
+      };
+      // O_t += P_t V over keys [64h, 64h+64) of block j: four K = 16 steps, P from TMEM
+      auto issue_pv = [&](int t, int slot, int j, int h) {
+        const uint64_t dv = dv0 + (uint64_t)(slot * kTile16);
+        const uint32_t tP = tb + C::kColS + t * kBlockN + h * kHalf;
+        const uint32_t tO = tb + C::kColO + t * D;
+        if (lead) {
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
             const int kk = 4 * h + k4;
-            umma_ts(tO, tP + kk * 8, dv + kk * (2048 / 16), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            umma_ts(tO, tP + k4 * 8, dv + kk * (2048 / 16), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
           }
-        };
-        // P written by the softmax warps' tcgen05.st: their wait::st, fence and arrive pair
-        // with this wait and the fence after it before an MMA reads P
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          const bool got = mbar_wait_bounded(bar, parity, abort, wait_ns);
-          if (got) tc_fence_after_sync();
-          return got;
-        };
-        // K, V written by the converters, whose proxy fence precedes their arrival
-        auto wait_tile = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort, wait_ns); };
-        int slot = 0, use = 0;  // ring position of the next tile, in consumption order
-        auto advance = [&]() {
-          if (++slot == C::kSlots) {
-            slot = 0;
-            use ^= 1;
-          }
-        };
-        bool ok = true;
-        if (alt) {
-          // alternate blocks: tile t takes blocks t, t + 2, ...; S_t = Q K(t)^T first, then
-          // for j = 0, 1, ...: PV of block j for tile j % 2 and that tile's next QK^T
-          for (int t = 0; t < kTiles && t < nbt && ok; ++t) {
-            ok = wait_tile(&bars->full[slot], use);
-            if (!ok) break;
-            issue_qk(t, slot);
-            umma_commit(&bars->empty[slot]);
-            advance();
-          }
-          for (int j = 0; j < nbt && ok; ++j) {
-            const int t = j & 1, i = j >> 1;  // tile and its own block count
-            ok = wait_tile(&bars->full[slot], use);  // V(j)
-            if (!ok) break;
-            const int sv = slot;
-            advance();
-            ok = wait(&bars->p_full[t][0], i & 1);
-            if (!ok) break;
-            issue_pv(t, sv, i, 0);
-            ok = wait(&bars->p_full[t][1], i & 1);
-            if (!ok) break;
-            issue_pv(t, sv, i, 1);
-            umma_commit(&bars->empty[sv]);
-            if (j + 2 < nbt) {
-              ok = wait_tile(&bars->full[slot], use);  // K(j + 2)
-              if (!ok) break;
-              issue_qk(t, slot);
-              umma_commit(&bars->empty[slot]);
-              advance();
-            } else if (t == 0) {
-              umma_commit(&bars->o_full[0]);  // tile 0's last PV; no QK^T follows it
+          umma_commit(&bars->pv_done[t]);
+        }
+      };
+      // P written by the softmax warps' tcgen05.st: their wait::st, fence and arrive pair
+      // with this wait and the fence after it before an MMA reads P
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, wait_ns));
+        tc_fence_after_sync();
+        return got;
+      };
+      // K, V written by the converters, whose proxy fence precedes their arrival
+      auto wait_tile = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, wait_ns));
+      };
+      int slot = 0, use = 0;  // ring position of the next tile, in consumption order
+      auto advance = [&]() {
+        if (++slot == C::kSlots) {
+          slot = 0;
+          use ^= 1;
+        }
+      };
+      bool ok = true;
+      if (by_turns) {
+        // alternate blocks: tile t takes blocks t, t + 2, ...; S_t = Q K(t)^T first, then
+        // for j = 0, 1, ...: PV of block j for tile j % 2 and that tile's next QK^T, by halves
+        for (int t = 0; t < kTiles && t < blocks && ok; ++t) {
+          ok = wait_tile(&bars->full[slot], use);
+          if (!ok) break;
+          issue_qk(t, slot, 0);
+          issue_qk(t, slot, 1);
+          commit(&bars->empty[slot]);
+          advance();
+        }
+        for (int j = 0; j < blocks && ok; ++j) {
+          const int t = j & 1, i = j >> 1;  // tile and its own block count
+          ok = wait_tile(&bars->full[slot], use);  // V(j)
+          if (!ok) break;
+          const int sv = slot;
+          advance();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(&bars->p_full[t][h], i & 1);
+            if (ok) issue_pv(t, sv, i, h);
+            if (ok && h == 1) commit(&bars->empty[sv]);
+            if (ok && j + 2 < blocks) {
+              if (h == 0) ok = wait_tile(&bars->full[slot], use);  // K(j + 2)
+              if (ok) issue_qk(t, slot, h);
             }
           }
-        }
-        if (ok && !alt) {
-          ok = wait_tile(&bars->full[slot], use);  // K(0)
-          if (ok) {
-            issue_qk(0, slot);
-            issue_qk(1, slot);
-            umma_commit(&bars->empty[slot]);
+          if (!ok) break;
+          if (j + 2 < blocks) {
+            commit(&bars->empty[slot]);
             advance();
+          } else if (t == 0) {
+            commit(&bars->o_full[0]);  // tile 0's last PV; no QK^T follows it
           }
         }
-        for (int j = 0; j < nbt && ok && !alt; ++j) {
+      } else {
+        ok = wait_tile(&bars->full[slot], use);  // K(0)
+        if (ok) {
+#pragma unroll
+          for (int x = 0; x < 2 * kTiles; ++x) issue_qk(x % kTiles, slot, x / kTiles);
+          commit(&bars->empty[slot]);
+          advance();
+        }
+        for (int j = 0; j < blocks && ok; ++j) {
           const int sv = slot, uv = use;  // V(j)
           advance();
-          const bool more = j + 1 < nbt;
+          const bool more = j + 1 < blocks;
           const int sk = slot, uk = use;  // K(j+1), when there is one
-          const uint32_t pp = j & 1;
           ok = wait_tile(&bars->full[sv], uv);
-          for (int t = 0; t < kTiles && ok; ++t) {
-            ok = wait(&bars->p_full[t][0], pp);
-            if (!ok) break;
-            issue_pv(t, sv, j, 0);
-            ok = wait(&bars->p_full[t][1], pp);
-            if (!ok) break;
-            issue_pv(t, sv, j, 1);
+#pragma unroll
+          for (int x = 0; x < 2 * kTiles; ++x) {  // halves, of each both tiles
+            const int h = x / kTiles, t = x % kTiles;
+            ok = ok && wait(&bars->p_full[t][h], j & 1);
+            if (ok) issue_pv(t, sv, j, h);
             // V(j) is free once both tiles' PV have read it: released before the next QK^T,
             // so that its refill (a few microseconds in flight) starts that much earlier
-            if (t == 1) umma_commit(&bars->empty[sv]);
-            if (!more && t == 0) umma_commit(&bars->o_full[0]);  // tile 0's epilogue may start
-            if (more) {
-              if (t == 0) ok = wait_tile(&bars->full[sk], uk);
-              if (!ok) break;
-              issue_qk(t, sk);
+            if (ok && x == 3) commit(&bars->empty[sv]);
+            if (ok && !more && x == 2) commit(&bars->o_full[0]);  // tile 0's epilogue may start
+            if (ok && more) {
+              if (x == 0) ok = wait_tile(&bars->full[sk], uk);
+              if (ok) issue_qk(t, sk, h);
             }
           }
           if (!ok) break;
           if (more) {
-            umma_commit(&bars->empty[sk]);
+            commit(&bars->empty[sk]);
             advance();
           }
         }
-        // tile 0's last PV precedes tile 1's in issue order, so o_full[1] completes last
-        umma_commit(&bars->o_full[1]);
-        drain_wait(&bars->o_full[1], 0);
       }
+      // tile 0's last PV precedes tile 1's in issue order, so o_full[1] completes last
+      commit(&bars->o_full[1]);
+      if (lead) drain_wait(&bars->o_full[1], 0);
       __syncwarp();
     } else {
       // ---------------------------------------------------------------- softmax / epilogue
@@ -777,59 +789,59 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
       bool ok = true;
       // blocks of this tile: all of them, or every other one (from block t) when alternating
       const int n_mine = alt ? (nbt - t + 1) / 2 : nbt;
-      for (int i = 0; i < n_mine; ++i) {
+      // Half a block at a time: while this warp works at one half, the tensor core computes the
+      // other half's next scores, so that neither waits for the other's turn.
+#pragma unroll 1
+      for (int n = 0; n < 2 * n_mine; ++n) {
+        const int i = n >> 1, h = n & 1;
         const int j = alt ? 2 * i + t : i;  // the block
         const int tb = j % kTables;
+        const uint32_t tH = tS + h * kHalf;
         // the block's scales first (they came long ago), then its scores
-        float ck[kGroups], cm[kGroups];
-        const bool scaled = mbar_wait_bounded(&bars->table_full[tb], (j / kTables) & 1, abort, wait_ns);
+        constexpr int kHG = kHalf / kGroup;  // groups of a half
+        float ck[kHG], cm[kHG], rv[kHG];
+        const bool scaled = h != 0 || mbar_wait_bounded(&bars->table_full[tb], (j / kTables) & 1, abort, wait_ns);
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
+        for (int g = 0; g < kHG; ++g) {
           // not 0 (a row or a block of zeros), so that a masked score stays -inf
-          ck[g] = fmaxf(bars->kc[tb][g] * cs, 1.17549435e-38f);
-          cm[g] = bars->lv[tb][g];
+          ck[g] = fmaxf(bars->kc[tb][kHG * h + g] * cs, 1.17549435e-38f);
+          cm[g] = bars->lv[tb][kHG * h + g];
+          rv[g] = bars->rv[tb][kHG * h + g];
         }
-        ok = __all_sync(0xffffffffu, scaled && mbar_wait_bounded(&bars->s_full[t], i & 1, abort, wait_ns));
+        ok = __all_sync(0xffffffffu, scaled && mbar_wait_bounded(&bars->s_full[t][h], i & 1, abort, wait_ns));
         if (!ok) break;
         tc_fence_after_sync();
-        int shift = 0;  // masked leading columns (this row)
-        if (win_rows && j < nb) shift = max(0, min(cut - (c.key_begin + j * kBlockN), kBlockN));
-        const int lim = j == nb - 1 ? tail_end : kBlockN;  // columns from here on are masked
-        const bool tree_blk = j == nb;                      // keys = the sequence's tree nodes
-        if (tree_blk && mask_tree_scores(bars->parent, tS, has_row ? node : -1)) bars->tree_err = 1u;
-        // All 128 scores for the row maximum; the first half stays in registers for its P.
-        float lo[kHalf];
-        float hi[kHalf];
-        float mx = -INFINITY;
+        float x[kHalf];
         {
-          uint32_t r[4][32];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, r[q]);
+          uint32_t r[2][32];
+          tmem_ld32(tH, r[0]);
+          tmem_ld32(tH + 32, r[1]);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < kHalf; ++e) {
-            lo[e] = __uint_as_float(r[e >> 5][e & 31]);
-            hi[e] = __uint_as_float(r[2 + (e >> 5)][e & 31]);
-          }
-          if (shift > 0 || lim < kBlockN) {  // the sequence's last prefix block, or a window's first
+          for (int e = 0; e < kHalf; ++e) x[e] = __uint_as_float(r[e >> 5][e & 31]);
+        }
+        if (j >= nb - 1 || win_rows) {  // the sequence's last prefix block, the tree's, or a window's first
+          if (j == nb) {  // keys = the sequence's tree nodes
+            if (!mask_tree_scores(bars->parent, x, has_row ? node : -1, h)) bars->tree_err = 1u;
+          } else {
+            const int shift = win_rows ? cut - (c.key_begin + j * kBlockN) - kHalf * h : 0;  // masked leading columns
+            const int lim = (j == nb - 1 ? tail_end : kBlockN) - kHalf * h;                  // and from here on
 #pragma unroll
-            for (int e = 0; e < kHalf; ++e) {
-              if (e < shift || e >= lim) lo[e] = -INFINITY;
-              if (e + kHalf < shift || e + kHalf >= lim) hi[e] = -INFINITY;
-            }
+            for (int e = 0; e < kHalf; ++e)
+              if (e < shift || e >= lim) x[e] = -INFINITY;
           }
+        }
+        float mx = -INFINITY;
 #pragma unroll
-          for (int g = 0; g < kGroups / 2; ++g) {
-            float m0 = lo[16 * g], m1 = hi[16 * g];
+        for (int g = 0; g < kHG; ++g) {
+          float m0 = fmax3(x[16 * g], x[16 * g + 1], x[16 * g + 2]), m1 = fmax3(x[16 * g + 3], x[16 * g + 4], x[16 * g + 5]);
 #pragma unroll
-            for (int e = 1; e < 15; e += 2) {
-              m0 = fmax3(m0, lo[16 * g + e], lo[16 * g + e + 1]);
-              m1 = fmax3(m1, hi[16 * g + e], hi[16 * g + e + 1]);
-            }
-            m0 = fmaxf(m0, lo[16 * g + 15]);
-            m1 = fmaxf(m1, hi[16 * g + 15]);
-            mx = fmax3(mx, fmaf(m0, ck[g], cm[g]), fmaf(m1, ck[g + 4], cm[g + 4]));
+          for (int e = 6; e < 14; e += 4) {
+            m0 = fmax3(m0, x[16 * g + e], x[16 * g + e + 1]);
+            m1 = fmax3(m1, x[16 * g + e + 2], x[16 * g + e + 3]);
           }
+          m0 = fmax3(m0, x[16 * g + 14], x[16 * g + 15]);
+          mx = fmaxf(mx, fmaf(fmaxf(m0, m1), ck[g], cm[g]));
         }
         const bool raise = mx > m + kRaise;
         const bool any_raise = __any_sync(0xffffffffu, raise);
@@ -838,13 +850,17 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         // keeps m = -inf; its P is 0 against any finite reference
         const float m_off = (m_new == -INFINITY ? 0.f : m_new) - kOff;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) cm[g] -= m_off;
+        for (int g = 0; g < kHG; ++g) cm[g] -= m_off;
         if (any_raise) {
-          // the maximum moved up: rescale what O_t and l hold. O_t is idle: every PV of
-          // this tile issued before S_t(j) has completed (s_full), and PV_t(j) waits for
-          // this warpgroup's P. f = 1 where m is unchanged, 0 before the first block.
+          // the maximum moved up: rescale what O_t and l hold. O_t is idle once the last
+          // half's PV has completed (those before it precede S_t in the tensor core's order),
+          // and this half's waits for this warpgroup's P. f = 1 where m is unchanged, 0
+          // before the first half.
           const float f = m == m_new ? 1.f : ex2_approx(m - m_new);
-          if (i > 0) {
+          if (n > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->pv_done[t], (n - 1) & 1, abort, wait_ns));
+            if (!ok) break;
+            tc_fence_after_sync();
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
               uint32_t o[16];
@@ -858,37 +874,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
           l *= f;
           m = m_new;
         }
-        {
-          uint32_t pk[kHalf / 2];
-          make_p(lo, ck, cm, bars->rv[tb], pk, l);
-          tmem_st32(tS, pk);  // P over keys 0..63 -> columns 0..31
-          tmem_wait_st();
-          tc_fence_before_sync();
-          mbar_arrive(&bars->p_full[t][0]);
-        }
-        {
-          // keys 64..127 are read again (P took columns 0..31 only, so their scores are
-          // intact): with both halves live the block's code spilled, and ran 9% longer
-          uint32_t r[2][32];
-          tmem_ld32(tS + 64, r[0]);
-          tmem_ld32(tS + 96, r[1]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < kHalf; ++e) hi[e] = __uint_as_float(r[e >> 5][e & 31]);
-          if (shift > kHalf || lim < kBlockN) {
-#pragma unroll
-            for (int e = 0; e < kHalf; ++e)
-              if (e + kHalf < shift || e + kHalf >= lim) hi[e] = -INFINITY;
-          }
-        }
-        {
-          uint32_t pk[kHalf / 2];
-          make_p(hi, ck + 4, cm + 4, bars->rv[tb] + 4, pk, l);
-          tmem_st32(tS + 32, pk);  // keys 64..127 -> columns 32..63
-          tmem_wait_st();
-          tc_fence_before_sync();
-          mbar_arrive(&bars->p_full[t][1]);
-        }
+        uint32_t pk[kHalf / 2];
+        make_p(x, ck, cm, rv, pk, l);
+        tmem_st32(tH, pk);  // over the half's scores
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&bars->p_full[t][h]);
       }
       // -------------------------------------------------------------- epilogue
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->o_full[t], 0, abort, wait_ns));
