@@ -98,9 +98,11 @@ struct Bars {
   uint64_t pv_done[kTiles];             // O_t holds one more half
   uint64_t o_full[kTiles];              // every MMA of tile t finished
   uint64_t tree_full;                   // tree_max is there
+  uint64_t mask_full;                   // the tree's Ancestors are, in raw tile mask_slot's place
   uint32_t tmem_base;
   uint32_t abort;
   uint32_t tree_err;                    // a parent link that is not a rooted tree's
+  int32_t mask_slot;
   float kc[kTables][kGroups];           // key scales of the block's groups
   float lv[kTables][kGroups];           // log2 of the value scales
   float rv[kTables][kGroups];           // 1 / value scale
@@ -214,35 +216,46 @@ __device__ __forceinline__ void make_p(const float (&s)[kHalf], const float* ck,
   }
 }
 
-// Tree mask (LongSpec, gist.science summary, section 2C, "Baum-Maskierung") of half h of the
-// tree block's scores x: key (tree node) y stays visible when y is the row's node or one of
-// its ancestors, found by following parent links. Every link is checked (node 0 is the root
-// with parent -1, any other node's parent lies below it), so the walk ends; false: a check
-// failed. node < 0 (a padding row) masks every key.
-__device__ __forceinline__ bool mask_tree_scores(const int16_t* parent, float (&x)[kHalf], int node, int h) {
-  uint32_t am[2] = {0u, 0u};
+// Tree mask (LongSpec, gist.science summary, section 2C, "Baum-Maskierung"): the nodes that
+// each of the tree's n nodes sees, itself and its ancestors, as bits, by one warp. Every link
+// is checked (node 0 is the root with parent -1, any other node's parent lies below it); false
+// in a lane that found a bad one, which then counts as a root. Seven rounds of pointer jumping
+// cover 128 levels; a lane's nodes are lane, lane + 32, ...: `up` and `seen` hold all of them
+// between rounds.
+struct Ancestors {
+  uint32_t seen[kMaxTree][4];
+  int32_t up[kMaxTree];
+};
+__device__ __forceinline__ bool find_ancestors(Ancestors* t, const int32_t* parent, int n, int lane) {
   bool good = true;
-  if (node >= 0) {
-    int y = node;
-    for (int step = 0; step <= kMaxTree; ++step) {
-      const uint32_t bit = (y >> 6) == h ? 1u << (y & 31) : 0u;
-      am[0] |= y & 32 ? 0u : bit;
-      am[1] |= y & 32 ? bit : 0u;
-      const int pp = parent[y];
-      if (y == 0) {
-        good = pp == -1;
-        break;
-      }
-      if (pp < 0 || pp >= y) {
-        good = false;
-        break;
-      }
-      y = pp;
-    }
-  }
+  for (int x = lane; x < kMaxTree; x += 32) {
+    const int pp = x < n ? parent[x] : -1;
+    const bool fine = x == 0 || x >= n ? pp == -1 : pp >= 0 && pp < x;
+    good &= fine;
+    t->up[x] = fine ? pp : -1;
 #pragma unroll
-  for (int e = 0; e < kHalf; ++e)
-    if (!((am[e >> 5] >> (e & 31)) & 1u)) x[e] = -INFINITY;
+    for (int w = 0; w < 4; ++w) t->seen[x][w] = x >> 5 == w ? 1u << (x & 31) : 0u;
+  }
+  __syncwarp();
+  for (int round = 0; round < 7; ++round) {
+    uint32_t more[kMaxTree / 32][4];
+    int32_t next[kMaxTree / 32];
+#pragma unroll
+    for (int q = 0; q < kMaxTree / 32; ++q) {
+      const int y = t->up[lane + 32 * q];
+      next[q] = y >= 0 ? t->up[y] : -1;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) more[q][w] = y >= 0 ? t->seen[y][w] : 0u;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < kMaxTree / 32; ++q) {
+      t->up[lane + 32 * q] = next[q];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) t->seen[lane + 32 * q][w] |= more[q][w];
+    }
+    __syncwarp();
+  }
   return good;
 }
 
@@ -328,6 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
   };
 
   if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_map(&P.tmap_q);
+    tma_prefetch_map(&P.tmap_k);
+    tma_prefetch_map(&P.tmap_v);
     mbar_init(&bars->q_full, 1);
     for (int s = 0; s < C::kRaw; ++s) {
       mbar_init(&bars->raw_full[s], 1);
@@ -347,23 +363,29 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
       mbar_init(&bars->o_full[t], 1);
     }
     mbar_init(&bars->tree_full, 8);
+    mbar_init(&bars->mask_full, 1);
     bars->tree_max[0] = bars->tree_max[1] = 0u;
     bars->abort = 0u;
     bars->tree_err = 0u;
     fence_mbar_init();
-    tma_prefetch_map(&P.tmap_q);
-    tma_prefetch_map(&P.tmap_k);
-    tma_prefetch_map(&P.tmap_v);
-    tma_prefetch_map(&P.tmap_o);
   }
   if (warp == kMmaWarp) {
+    if (lane == 0) tma_prefetch_map(&P.tmap_o);
+    __syncwarp();
     tmem_alloc(&bars->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
+  // The producer, which made the barriers, does not wait for the others to see them: its first
+  // loads are on their way meanwhile.
   tc_fence_before_sync();
-  __syncthreads();
+  if (warp == kProducerWarp) {
+    __syncwarp();
+    asm volatile("bar.arrive 4, 384;" ::: "memory");
+  } else {
+    asm volatile("bar.sync 4, 384;" ::: "memory");
+  }
   tc_fence_after_sync();
-  const uint32_t tbase = bars->tmem_base;
+  const uint32_t tbase = warp == kProducerWarp ? 0u : bars->tmem_base;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == kProducerWarp) {
@@ -443,6 +465,17 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
       }
     }
     put_scales();
+    if (has_tree && ok) {  // where the next raw tile would go
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->raw_empty[slot], (use & 1) ^ 1, abort, wait_ns));
+      if (ok) {
+        Ancestors* t = reinterpret_cast<Ancestors*>(smem + C::kRawOff + slot * C::kRawBytes);
+        if (!find_ancestors(t, a.parent + tree_base, tree_n, lane)) bars->tree_err = 1u;
+        if (lane == 0) {
+          bars->mask_slot = slot;
+          mbar_arrive(&bars->mask_full);
+        }
+      }
+    }
     if (!q_issued) {  // no prefix tile at all
       wait_prior();
       if (lane == 0) {
@@ -567,20 +600,23 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         // the largest magnitudes of the tree block's keys and values, while Q and the first
         // keys are on their way
         wait_prior();
+        constexpr int kChunks = D / 8;
+        uint4 w[2][kChunks / 2];  // 128 rows over 256 threads
 #pragma unroll
         for (int val = 0; val < 2; ++val) {
-          constexpr int kChunks = D / 8;
           const uint16_t* from = (val ? a.v_tree : a.k_tree) + ((size_t)tree_base * p.Hkv + c.kh) * D;
-          uint32_t m[4] = {0u, 0u, 0u, 0u};
-          uint4 w[kChunks / 2];  // 128 rows over 256 threads
 #pragma unroll
           for (int e = 0; e < kChunks / 2; ++e) {
             const int i = tid + 256 * e, row = i / kChunks;
-            w[e] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < tree_n) w[e] = *reinterpret_cast<const uint4*>(from + (size_t)row * p.Hkv * D + i % kChunks * 8);
+            w[val][e] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < tree_n) w[val][e] = *reinterpret_cast<const uint4*>(from + (size_t)row * p.Hkv * D + i % kChunks * 8);
           }
+        }
 #pragma unroll
-          for (int e = 0; e < kChunks / 2; ++e) take_max(m, w[e]);
+        for (int val = 0; val < 2; ++val) {
+          uint32_t m[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int e = 0; e < kChunks / 2; ++e) take_max(m, w[val][e]);
           const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(join_max(m)));
           if (lane == 0) atomicMax(&bars->tree_max[val], most);
         }
@@ -608,9 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
           *reinterpret_cast<uint4*>(line + (i / 8) * C::kQPanelBytes + (((i + lane) & 7) << 4)) = f16_of_bf16(w[i], mul);
       }
       fence_proxy_async_smem();
-      // the tree of the sequence, for the tree mask; a parent outside [-1, T) is stored
+      // the tree of the sequence, for the rows' depths; a parent outside [-1, T) is stored
       // as a value that fails the walk's checks
-      if (has_tree || win_rows) {
+      if (win_rows) {
         for (int x = tid; x < tree_n; x += 256) {
           const int32_t pp = a.parent[(size_t)tree_base + x];
           bars->parent[x] = (int16_t)(pp >= -1 && pp < tree_n ? pp : kMaxTree);
@@ -821,8 +857,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
           for (int e = 0; e < kHalf; ++e) x[e] = __uint_as_float(r[e >> 5][e & 31]);
         }
         if (j >= nb - 1 || win_rows) {  // the sequence's last prefix block, the tree's, or a window's first
-          if (j == nb) {  // keys = the sequence's tree nodes
-            if (!mask_tree_scores(bars->parent, x, has_row ? node : -1, h)) bars->tree_err = 1u;
+          if (j == nb) {  // keys = the sequence's tree nodes; a padding row sees none
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->mask_full, 0, abort, wait_ns));
+            if (!ok) break;
+            const Ancestors* t = reinterpret_cast<const Ancestors*>(smem + C::kRawOff + bars->mask_slot * C::kRawBytes);
+            const uint32_t am[2] = {has_row ? t->seen[node][2 * h] : 0u, has_row ? t->seen[node][2 * h + 1] : 0u};
+#pragma unroll
+            for (int e = 0; e < kHalf; ++e)
+              if (!((am[e >> 5] >> (e & 31)) & 1u)) x[e] = -INFINITY;
           } else {
             const int shift = win_rows ? cut - (c.key_begin + j * kBlockN) - kHalf * h : 0;  // masked leading columns
             const int lim = (j == nb - 1 ? tail_end : kBlockN) - kHalf * h;                  // and from here on
