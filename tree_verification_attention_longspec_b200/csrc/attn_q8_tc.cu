@@ -501,11 +501,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     for (int ld = 0; ld < n_tiles && ok; ++ld) {
       int j, val;
       tile_of(ld, &j, &val);
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->empty[slot], (use & 1) ^ 1, abort, wait_ns));
-      if (!ok) break;
+      auto wait_slot = [&]() {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(&bars->empty[slot], (use & 1) ^ 1, abort, wait_ns));
+      };
       uint8_t* dst = smem + C::kSlotOff + slot * C::kTileBytes;
       if (j < nb) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->raw_full[raw], raw_use & 1, abort, wait_ns));
+        ok = wait_slot() && __all_sync(0xffffffffu, mbar_wait_bounded(&bars->raw_full[raw], raw_use & 1, abort, wait_ns));
         if (!ok) break;
         const uint8_t* src = smem + C::kRawOff + raw * C::kRawBytes;
         const int lim = j == nb - 1 ? tail_end : kBlockN;
@@ -547,9 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         }
       } else {
         // The tree block: bf16 rows from global memory, times a power of two for the tile (its
-        // largest magnitude has been found by the softmax warps).
+        // largest magnitude has been found by the softmax warps). The first half of the rows is
+        // on its way before the tile's place is free.
         constexpr int kChunks = D / 8;  // 16-byte chunks of a bf16 row
-        constexpr int kIter = 128 * kChunks / kConverters, kBatch = 8;
+        constexpr int kIter = 128 * kChunks / kConverters, kBatch = kIter / 2;
         if (!val) {
           wait_prior();
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->tree_full, 0, abort, wait_ns));
@@ -573,6 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
             w[e] = make_uint4(0u, 0u, 0u, 0u);
             if (row < tree_n) w[e] = *reinterpret_cast<const uint4*>(from + (size_t)row * p.Hkv * D + i % kChunks * 8);
           }
+          if (it == 0) ok = wait_slot();
+          if (!ok) break;
 #pragma unroll
           for (int e = 0; e < kBatch; ++e) {
             const int i = ct + (it + e) * kConverters, row = i / kChunks, cc = i % kChunks;
@@ -580,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
                 f16_of_bf16(w[e], mul);
           }
         }
+        if (!ok) break;
       }
       fence_proxy_async_smem();  // the tile is read by the tensor core
       __syncwarp();
