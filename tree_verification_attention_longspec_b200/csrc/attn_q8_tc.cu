@@ -548,10 +548,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         }
       } else {
         // The tree block: bf16 rows from global memory, times a power of two for the tile (its
-        // largest magnitude has been found by the softmax warps). The first half of the rows is
-        // on its way before the tile's place is free.
+        // largest magnitude has been found by the softmax warps). The first rows are on their
+        // way before the tile's place is free. Keys past the tree are masked whatever they
+        // hold; values there become zeros.
         constexpr int kChunks = D / 8;  // 16-byte chunks of a bf16 row
-        constexpr int kIter = 128 * kChunks / kConverters, kBatch = kIter / 2;
+        constexpr int kIter = 128 * kChunks / kConverters, kBatch = 8;
+        const int used = (tree_n * kChunks + kConverters - 1) / kConverters;  // of the iterations
         if (!val) {
           wait_prior();
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars->tree_full, 0, abort, wait_ns));
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         if (first_warp && !val) write_scales(j, pow2f(-ksh), (float)-vsh, pow2f(vsh));  // all groups alike
         const float mul = pow2f(val ? vsh : ksh);
 #pragma unroll 1
-        for (int it = 0; it < kIter; it += kBatch) {
+        for (int it = 0; it < used; it += kBatch) {
           uint4 w[kBatch];
 #pragma unroll
           for (int e = 0; e < kBatch; ++e) {
@@ -585,6 +587,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
           }
         }
         if (!ok) break;
+        if (val) {
+#pragma unroll 1
+          for (int it = (used + kBatch - 1) / kBatch * kBatch; it < kIter; ++it) {
+            const int i = ct + it * kConverters, row = i / kChunks, cc = i % kChunks;
+            *reinterpret_cast<uint4*>(dst + (cc / 8) * C::kPanelBytes + row * 128 + (((cc % 8) ^ (row & 7)) << 4)) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
       }
       fence_proxy_async_smem();  // the tile is read by the tensor core
       __syncwarp();
