@@ -171,6 +171,24 @@ def test_top_k_that_ends_below_zero_with_tiny_logits_above(small, few):
         _check(*_sample(rows, r.random(40), dtype, top_k=np.full(40, 2000 + few + 500), top_p=p))
 
 
+@pytest.mark.parametrize("vocab", [4000, 40000])
+def test_borders_above_among_and_below_small_logits(vocab):
+    """bf16 rows with zeros and logits too small to have a bin of their own, and thresholds of
+    each kind on either side of them and among them."""
+    r = np.random.default_rng(vocab)
+    n = 48
+    x = r.standard_normal((n, vocab)) * r.choice([0.3, 2.0], (n, 1))
+    few = r.random((n, vocab)) < r.choice([0.001, 0.01, 0.3], (n, 1))
+    x = np.where(few, r.choice([0.0, -0.0, 1e-5, -1e-5, 3e-4, -3e-4, 1e-30], (n, vocab)), x)
+    half = (x > 1e-3).sum(1)
+    low = (x > -1e-3).sum(1)
+    at = r.choice([0.5, 0.9, 1.0, 1.02, 1.1, 1.5], n)
+    for k in (np.zeros(n), half * at, low * at, np.full(n, 10)):
+        for p in (np.ones(n), r.uniform(0.3, 1.0, n), np.full(n, 0.995)):
+            for m in (np.zeros(n), np.exp(-x.max(1)) * r.choice([0.9, 1.0, 1.1], n)):
+                _check(*_sample(x, r.random(n), "bf16", top_k=k.astype(int), top_p=p, min_p=m))
+
+
 @pytest.mark.parametrize("scale", [0.1, 3.0, 12.0, 40.0])
 def test_logits_inside_and_outside_the_plain_bins(scale):
     """bf16 logits below and above 32 in magnitude, and runs of small ones."""

@@ -357,8 +357,8 @@ class Sampler {
     if constexpr (!F32) {
       if (cuts) {
         KeyMap map;
-        if (counted && plain_map(t, &map)) {
-          if (resolve_keys(map, k, p, least, u)) return;
+        if (counted) {
+          if (plain_map(t, &map) && resolve_keys(map, k, p, least, u)) return;
           cl_.sync();
         }
         if (key_map(t, &map)) {
@@ -933,8 +933,8 @@ class Sampler {
   // the histogram exact: thresholds and sums come from counts times weights, without a list,
   // and what is left to do for the entries themselves is to add up the kept ones' weights by
   // runs, from a table, in the one CTA that holds the token. Smaller magnitudes have no bin:
-  // their few entries' weights are added up one by one, which does as long as the threshold
-  // lies above 0; else `resolve` decides.
+  // their few entries' weights are added up one by one, which does unless the threshold falls
+  // among them; then `resolve` decides.
   //
   // Bins for magnitudes from 2^-11 to 32 (`plain`) ask for no largest logit, so rows inside
   // are counted while they arrive; others once it is known, in bins below it (`key_map`).
@@ -953,6 +953,8 @@ class Sampler {
       const int neg = (int)(u << 16) >> 31;
       return ((int)(u & 0x7fffu) ^ ~neg) + (neg ? neg0 : ptop + 1);
     }
+    __device__ __forceinline__ int after_tiny() const { return zero >= 0 ? zero + 1 : pos; }  // bins below those without one
+    __device__ __forceinline__ float tiny_end() const { return __uint_as_float((uint32_t)least << 16); }  // their magnitudes are less
     __device__ __forceinline__ float value(int b) const {
       if (b < pos) return __uint_as_float((uint32_t)(ptop - b) << 16);
       return b == zero ? 0.f : -__uint_as_float((uint32_t)(b - neg0) << 16);
@@ -1071,15 +1073,21 @@ class Sampler {
   __device__ void count_all(const KeyMap& map) {
     uint32_t* hist = sh_.k.hist;
     for (int i = tid_; i < kKeys / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid_ == 0) sh_.tiny = 0ull;
+    if (tid_ == 0) {
+      sh_.tiny = 0ull;
+      sh_.k.n_tiny = 0u;
+    }
     __syncthreads();
     u64 tiny = 0;
+    uint32_t n_tiny = 0;
     auto count = [&](uint32_t bits) {
       const int b = map.bin(bits);
-      if ((uint32_t)b < (uint32_t)map.count)
+      if ((uint32_t)b < (uint32_t)map.count) {
         atomicAdd(&hist[b], 1u);
-      else if (b == -1)
+      } else if (b == -1) {
         tiny += weight(__uint_as_float(bits << 16));
+        ++n_tiny;
+      }
     };
     each_words(
         [&](const uint4& v) {
@@ -1104,6 +1112,7 @@ class Sampler {
         },
         [&](float x) { count(__float_as_uint(x) >> 16); });
     if (tiny) atomicAdd(&sh_.tiny, tiny);
+    if (n_tiny) atomicAdd(&sh_.k.n_tiny, n_tiny);
     cl_.sync();
   }
 
@@ -1154,7 +1163,8 @@ class Sampler {
     const float least_f = least > 0u ? of_key(least) : -INFINITY, edge = o.edge;
     const uint32_t cut = edge >= least_f ? o.m : 0u;  // of the edge's own entries, the first `cut` are kept
     {  // this CTA's kept weight but for the edge's entries, and their number
-      u64 keep = 0;
+      // (those without a bin are kept all or none: `ok` says so)
+      u64 keep = tid_ == 0 && whole >= map.after_tiny() && least_f <= -map.tiny_end() ? sh_.tiny : 0ull;
       auto four = [&](uint4 v, int b) {
 #pragma unroll 1  // (code that runs once costs its fetching)
         for (int e = 0; e < 4; ++e, ++b) {
@@ -1210,7 +1220,7 @@ class Sampler {
     __syncthreads();
     auto weight_at = [&](float x) {
       const int b = map.bin(__float_as_uint(x) >> 16);
-      return b < kTable ? sh_.k.weight[b] : (double)weight(x);
+      return (uint32_t)b < (uint32_t)kTable ? sh_.k.weight[b] : (double)weight(x);
     };
     double keep = 0.0;
     uint32_t equal = 0;
@@ -1305,20 +1315,31 @@ class Sampler {
   __device__ void look_keys(const KeyMap& map, uint32_t k, float p, uint32_t least, float u) {
     const int groups = kThreads / size_;  // of a CTA
     const Shared* o = cl_.map_shared_rank(&sh_, tid_ / groups);
-    u64 mass = o->k.mass[tid_ % groups], tiny = 0;
+    const u64 bins = o->k.mass[tid_ % groups];
+    u64 tiny = 0;
+    uint32_t n_tiny = 0;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
-      if (r < size_) tiny += cl_.map_shared_rank(&sh_, r)->tiny;
+      if (r < size_) {
+        const Shared* q = cl_.map_shared_rank(&sh_, r);
+        tiny += q->tiny;
+        n_tiny += q->k.n_tiny;
+      }
+    // The entries without a bin count to the group of the bin after them (if there is none, to
+    // the end): a border among them is not found there.
+    const int bt = map.after_tiny(), gt = bt / kKeysPer;
+    u64 mass = bins + (tid_ == gt ? tiny : 0ull), end = gt >= kThreads ? tiny : 0ull;
     // of group g, lane e's bin: its entries, and (none where there are none) their weight
     auto count_of = [&](int g) {
       return lane_ < kKeysPer ? cl_.map_shared_rank(&sh_, g / groups)->k.hist[kKeysPer * g + lane_] : 0u;
     };
     // top-k's border: bins before bk are kept whole, `room` entries of it
-    int bk = kKeys;  // none: the entries with a bin are fewer
+    int bk = kKeys;  // none: there are fewer entries
     uint32_t room = 0;
+    bool found = true;
     if (tid_ == 0) sh_.bins[0] = sh_.bins[1] = kThreads;  // the borders' groups
     if (k > 0) {
-      uint32_t own = 0;
+      uint32_t own = tid_ == gt ? n_tiny : 0u;
 #pragma unroll
       for (int e = 0; e < kKeysPer / 4; ++e) {
         const uint4 v = reinterpret_cast<const uint4*>(o->k.hist)[tid_ * (kKeysPer / 4) + e];
@@ -1336,18 +1357,25 @@ class Sampler {
       __syncthreads();
       const int g = (int)sh_.bins[0];
       if (g < kThreads) {
-        const uint32_t c = count_of(g), upto = warp_scan(c, lane_), left = sh_.cut;  // of the group
+        const int b = kKeysPer * g + lane_;
+        const bool past = g == gt && b >= bt;  // lanes after the entries without a bin
+        const uint32_t c = count_of(g), upto = warp_scan(c, lane_) + (past ? n_tiny : 0u), left = sh_.cut;  // of the group
         const int e = __ffs(__ballot_sync(0xffffffffu, upto >= left)) - 1;
+        const uint32_t first = __shfl_sync(0xffffffffu, upto - c, e);
+        const bool over = __shfl_sync(0xffffffffu, past ? 1 : 0, e);
+        found = left > first;
         bk = kKeysPer * g + e;
-        room = left - __shfl_sync(0xffffffffu, upto - c, e);
+        room = left - first;
         if (warp_ == g / 32) {  // its weight is what is kept of it
           const uint32_t kept = lane_ < e ? c : lane_ == e ? room : 0u;
-          const u64 w = warp_sum64(kept ? kept * weight(map.value(kKeysPer * g + lane_)) : 0ull);
-          if (tid_ == g) mass = w;
+          const u64 w = warp_sum64(kept ? kept * weight(map.value(b)) : 0ull);
+          if (tid_ == g) mass = w + (over ? tiny : 0ull);
         }
         if (tid_ > g) mass = 0;
+        end = 0;
+      } else if (n_tiny > 0u && gt >= kThreads) {
+        found = false;  // maybe among them
       }
-      if (bk < map.pos) tiny = 0;  // top-k ends above them
     } else {
       __syncthreads();
     }
@@ -1355,7 +1383,7 @@ class Sampler {
     if (lane_ == 31) sh_.scan[warp_] = minc;
     __syncthreads();
     const u64 sums = lane_ < kWarps ? sh_.scan[lane_] : 0ull, upto = warp_scan(sums, lane_);
-    const u64 all = __shfl_sync(0xffffffffu, upto, kWarps - 1) + tiny;
+    const u64 all = __shfl_sync(0xffffffffu, upto, kWarps - 1) + end;
     const u64 before = __shfl_sync(0xffffffffu, upto - sums, warp_) + minc - mass;
     u64 goal = all;  // the border holds the goal-th unit of weight: the last kept
     if (p < 1.0f) {
@@ -1366,37 +1394,35 @@ class Sampler {
       sh_.bins[1] = (uint32_t)tid_;
       sh_.above = before;
     }
+    if (tid_ == 0) sh_.keys.ok = 0;
     __syncthreads();
     const int g = (int)sh_.bins[1];
-    if (g == kThreads) {  // among the entries without a bin
-      if (tid_ == 0) sh_.keys.ok = 0;
-      return;
-    }
+    if (g == kThreads || !found) return;
+    const float least_f = least > 0u ? of_key(least) : -INFINITY;
     const int b = kKeysPer * g + lane_;
     if (warp_ == 0) {
       uint32_t c = count_of(g);
       if (b >= bk) c = b == bk ? room : 0u;
-      const u64 w = c ? weight(map.value(b)) : 0ull, at = sh_.above + warp_scan(c * w, lane_) - c * w;
+      const u64 w = c ? weight(map.value(b)) : 0ull, extra = g == gt && b >= bt && bk >= bt ? tiny : 0ull;
+      const u64 at = sh_.above + extra + warp_scan(c * w, lane_) - c * w;
       if (at < goal && goal <= at + c * w) {
         uint32_t m = (uint32_t)((float)(goal - at) / (float)w);  // off by less than one: at most 2^20
         while (m * w < goal - at) ++m;
         while (m > 1u && (m - 1u) * w >= goal - at) --m;
         const u64 z = at + m * w;  // kept, but for min-p
-        // entries without a bin lie among those of the zero: they matter neither to a border
-        // above it nor, where top-k ends above them too, to its sums
-        const int ok = tiny == 0ull || (b < map.pos && k == 0) ? 1 : 0;
-        sh_.keys = KeyVerdict{target_of(u, z), w, map.value(b), m, (uint32_t)b, ok};
+        // no border among the entries without a bin: top-p's at a zero between them, or min-p's
+        const bool amid = b == map.zero || (b >= bt && least_f > -map.tiny_end() && least_f < map.tiny_end());
+        sh_.keys = KeyVerdict{target_of(u, z), w, map.value(b), m, (uint32_t)b, n_tiny == 0u || !amid ? 1 : 0};
       }
     }
     if (least == 0u) return;
     __syncthreads();
-    const float least_f = of_key(least);
     if (!sh_.keys.ok || sh_.keys.edge >= least_f) return;
     // min-p ends before the border: the bins down to it, of the groups before the border's whole
-    u64 kept = 0;
+    u64 kept = tid_ == 0 && (int)sh_.keys.bin >= bt && least_f <= -map.tiny_end() ? tiny : 0ull;
     if (tid_ <= g && map.value(kKeysPer * tid_) >= least_f) {
       if (tid_ < g && map.value(kKeysPer * tid_ + kKeysPer - 1) >= least_f) {
-        kept = mass;
+        kept += bins;
       } else {
 #pragma unroll 1
         for (int e = 0; e < kKeysPer; ++e) {
