@@ -1214,13 +1214,23 @@ class Sampler {
         }
       }
     if (owner != rank_) return true;
-    // weights of the bins kept whole, where the histogram was
-    const int from = top_ > 0.f ? map.ptop - (int)(__float_as_uint(top_) >> 16) : map.pos;  // bins above hold nothing
-    for (int b = from + tid_; b < min(whole, kTable); b += kThreads) sh_.k.weight[b] = (double)weight(map.value(b));
+    // Weights of the values kept whole, where the histogram was: those above a positive edge, or
+    // above a negative one but for the smallest magnitudes, as many as there is room for.
+    const int tm = top_ > 0.f ? (int)(__float_as_uint(top_) >> 16) : 0;
+    const int em = (int)(__float_as_uint(fabsf(edge)) >> 16);
+    KeyMap tab{tm, tm - em, -1, 0, 0, tm - em <= kTable ? tm - em : 0};  // of a positive edge
+    if (!(edge > 0.f)) {
+      // the least magnitude in it: those from it to the top's and to the edge's have room
+      const int least_mag = max(max(1, max(tm, em) - kTable + 1),
+                                top_ > 0.f ? (tm + em + 3 - kTable) / 2 : (int)(__float_as_uint(-top_) >> 16 & 0x7fffu));
+      const int pos = top_ > 0.f ? max(0, tm - least_mag + 1) : 0;
+      tab = KeyMap{tm, pos, -1, pos - least_mag, least_mag, edge < 0.f ? pos + max(0, em - least_mag + 1) : 0};
+    }
+    for (int b = tid_; b < tab.count; b += kThreads) sh_.k.weight[b] = (double)weight(tab.value(b));
     __syncthreads();
-    auto weight_at = [&](float x) {
-      const int b = map.bin(__float_as_uint(x) >> 16);
-      return (uint32_t)b < (uint32_t)kTable ? sh_.k.weight[b] : (double)weight(x);
+    auto weight_at = [&](float x) {  // of x > edge
+      const int b = tab.bin(__float_as_uint(x) >> 16);
+      return (uint32_t)b < (uint32_t)tab.count ? sh_.k.weight[b] : (double)weight(x);
     };
     double keep = 0.0;
     uint32_t equal = 0;
@@ -1235,18 +1245,35 @@ class Sampler {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           const uint32_t m2 = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
           if (!(fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u)) >= low)) return;
-          if (whole > kTable || edge <= 0.f) {  // past the table, or values around 0 among the kept
+          bool slow = tab.count == 0;  // not all in the table
+          if (tab.least > 0) {
+            uint32_t small = 0x7fff7fffu;
 #pragma unroll
+            for (int e = 0; e < 4; ++e) small = __vminu2(small, w[e] & 0x7fff7fffu);
+            slow |= min(small & 0xffffu, small >> 16) < (uint32_t)tab.least;
+          }
+          if (slow) {
+#pragma unroll 1
             for (int e = 0; e < 4; ++e) {
-              add(__uint_as_float(w[e] << 16));
-              add(__uint_as_float(w[e] & 0xffff0000u));
+              const uint32_t x = e == 0 ? w[0] : e == 1 ? w[1] : e == 2 ? w[2] : w[3];
+              add(__uint_as_float(x << 16));
+              add(__uint_as_float(x & 0xffff0000u));
             }
-          } else {  // kept values are positive: a bin is the distance of their bits from the largest's
+          } else if (tab.least == 0) {  // positive ones only
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float x = __uint_as_float(w[e] << 16), y = __uint_as_float(w[e] & 0xffff0000u);
-              add_above(keep, table + 8u * (uint32_t)(map.ptop - (int)(w[e] & 0xffffu)), x, edge, least_f);
-              add_above(keep, table + 8u * (uint32_t)(map.ptop - (int)(w[e] >> 16)), y, edge, least_f);
+              add_above(keep, table + 8u * (uint32_t)(tm - (int)(w[e] & 0xffffu)), x, edge, least_f);
+              add_above(keep, table + 8u * (uint32_t)(tm - (int)(w[e] >> 16)), y, edge, least_f);
+              equal += x == edge ? 1u : 0u;
+              equal += y == edge ? 1u : 0u;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = __uint_as_float(w[e] << 16), y = __uint_as_float(w[e] & 0xffff0000u);
+              add_above(keep, table + 8u * (uint32_t)tab.large_bin(w[e] & 0xffffu), x, edge, least_f);
+              add_above(keep, table + 8u * (uint32_t)tab.large_bin(w[e] >> 16), y, edge, least_f);
               equal += x == edge ? 1u : 0u;
               equal += y == edge ? 1u : 0u;
             }
