@@ -48,10 +48,13 @@ def _refuse(t, name: str, dtypes, device, shape):
 def _ptr(t, name: str, dtype, device, shape=None):
     """The address of a dense CUDA tensor of this dtype, device and shape, or an error that
     names it. (One test on the way that every call takes: small calls are bound by it.)"""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device.index
-            or not t.is_contiguous() or shape is not None and t.shape != shape):
-        _refuse(t, name, (dtype,), device, shape)
-    return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.get_device() == device.index and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, (dtype,), device, shape)
 
 
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
@@ -226,7 +229,7 @@ class _AttnQ8:
         else:
             op = _ptr(out, "out", torch.bfloat16, dev, q_shape)
         if lse is None:
-            lse = torch.empty(lse_shape, dtype=torch.float32, device=dev)
+            lse = torch.empty_like(self._lse_like)
             lp = lse.data_ptr()
         else:
             lp = _ptr(lse, "lse", torch.float32, dev, lse_shape)
@@ -234,6 +237,8 @@ class _AttnQ8:
 
     def _shapes_of(self, rows):
         d = self.dims
+        # one element seen as many: what empty_like (half the cost of empty) takes its shape from
+        self._lse_like = torch.empty((), dtype=torch.float32, device=self.device).expand(rows, d.num_q_heads)
         return ((rows, d.num_q_heads, d.head_dim), (rows, d.num_q_heads), (d.batch + 1,),
                 (rows, d.num_kv_heads, d.head_dim))
 
@@ -327,7 +332,7 @@ def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=N
     rows, vocab, stride, u, kind, opts, keep = _sampling(logits, uniform, temperature, top_k, top_p, min_p, False)
     dev = logits.device
     if out is None:
-        out = torch.empty((rows,), dtype=torch.int32, device=dev)
+        out = torch.empty_like(uniform, dtype=torch.int32)
     _call(dev, "ls_sample", load_library().ls_sample, logits.data_ptr(), stride, u, ctypes.byref(opts),
           _ptr(out, "out", torch.int32, dev, (rows,)), rows, vocab, kind)
     return out
@@ -356,10 +361,10 @@ def tree_accept_sample(logits, uniform, tree_tokens, tree_parent, tree_size: int
             raise ValueError(f"{rows} rows of logits are not whole trees of {tree_size} nodes")
     tok = _ptr(tree_tokens, "tree_tokens", torch.int32, dev, (rows,))
     par = _ptr(tree_parent, "tree_parent", torch.int32, dev, (rows,))
-    node_token = torch.empty((rows,), dtype=torch.int32, device=dev)
+    node_token = torch.empty_like(tree_tokens)
     accept_path = torch.empty((batch, tree_size), dtype=torch.int32, device=dev)
     accept_len = torch.empty((batch,), dtype=torch.int32, device=dev)
-    next_token = torch.empty((batch,), dtype=torch.int32, device=dev)
+    next_token = torch.empty_like(accept_len)
     dims = binding.AcceptDims(batch, tree_size, vocab, kind)
     _call(dev, "ls_tree_accept_sample", load_library().ls_tree_accept_sample, logits.data_ptr(), u,
           ctypes.byref(opts), tok, par, trees, rows, node_token.data_ptr(), accept_len.data_ptr(),
