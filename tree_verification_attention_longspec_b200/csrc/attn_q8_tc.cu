@@ -26,14 +26,29 @@
 //                   instruction; rows past the sequence become zeros, so that whatever they
 //                   hold meets weight 0 as 0), and the tree's keys and values from
 //                   global memory
-// Measured (B200): 64 nodes, 28 heads over 4, 65,536 tokens: 88 us for both launches of the
-// call, 680 TFLOP/s, 0.42 of the measured bf16 rate; 64 nodes over 16,384 tokens: 39 us. A
-// pair of 128-key blocks takes some 5,000 cycles where its products need 2,050: the softmax
-// warps (about 1,000 instructions a warp and block) and the converters (about 700 a warp and
-// block, there being no 8-bit operand for K without Q and P in 8 bits too) share the issue
-// slots, and the two tiles run nearly in phase. Tried, and slower here: exponentials by
-// polynomial on the FMA pipe (126 us then, 137 with), registers moved from the converters to
-// the softmax (428 us: the converters spill), four converter warps.
+// By halves. S, P and the running maximum go by 64 keys: while a tile's softmax works at one
+// half of its scores, the tensor core replaces the other, whose P it has used (O_t += P V of
+// that half, then Q K^T of the next block's into its place), so neither waits for the other's
+// turn. Whole blocks at a time left every softmax warp idle for half the period. (Q K^T at
+// N = 64 reads Q twice as often; the tensor core has the time.) A raise of the maximum, rare,
+// waits for the last half's product before it rescales O_t.
+// Issue. All lanes of the MMA warp go along and one issues, so that descriptors stay in uniform
+// registers: from one lane's an MMA took 60 cycles to issue, and the issuer was what bound the
+// kernel (107 us against 84.5).
+//
+// Rings. A block holds its V and the next K for its whole length, so two more f16 tiles let the
+// converters run a block ahead; the raw ring gets what is left (three and four: 82.5 us, four
+// and two: 80.9).
+//
+// Measured (B200): 64 nodes, 28 heads over 4, 65,536 tokens: 81 us for both launches of the
+// call, 740 TFLOP/s, 0.45 of the measured bf16 rate; 64 nodes over 16,384 tokens: 37 us. A
+// half takes a softmax warp some 1,700 cycles, in which its SM quarter's two warps issue twice
+// 430 instructions and 64 exponentials a row (1,024 cycles of the MUFU), and two quarters a
+// converter's 350 (there being no 8-bit operand for K without Q and P in 8 bits too). Tried,
+// and no faster here: an eighth to a third of the exponentials by polynomial on the FMA pipe
+// (84.9 to 86 from 84.5), a higher threshold of raises (no change), registers moved from the converters to the softmax (428: the
+// converters spill), four converter warps. The converter's loop is not unrolled: the roles
+// share the code cache (92 us with, 88 without).
 // Every wait is bounded; on a timeout the CTA raises an abort flag, all roles drain their
 // in-flight copies and MMAs, TMEM is freed, and the chunk status reports it.
 #include <cudaTypedefs.h>
@@ -66,8 +81,8 @@ struct Cfg {
   static constexpr int kPanelBytes = 128 * 128;             // 128 rows x 64 f16, 128B-swizzled
   static constexpr int kTileBytes = kPanels * kPanelBytes;  // 128 rows x D f16
   static constexpr int kRawBytes = 128 * D;                 // 128 rows x D codes
-  static constexpr int kSlots = D == 128 ? 3 : 6;           // f16 tiles
-  static constexpr int kRaw = D == 128 ? 4 : 8;             // raw tiles
+  static constexpr int kSlots = D == 128 ? 4 : 6;           // f16 tiles
+  static constexpr int kRaw = D == 128 ? 2 : 8;             // raw tiles
   // Q: [panel][kUnitRows rows][128 B]; tile t is rows [128 t, 128 t + 128) of each panel
   static constexpr int kQPanelBytes = kUnitRows * 128;
   static constexpr int kQOff = 0;
