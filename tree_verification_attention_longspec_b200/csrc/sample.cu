@@ -345,6 +345,7 @@ class Sampler {
       auto first = [top](float x, uint32_t) { return x == top ? 1ull : 0ull; };
       u64 before;
       sums(first, &before);
+      leave();
       const int i = find(first, before, 0ull, w0_, w1_, sh_.wsum[warp_]);
       if (i >= 0) a_.out[row_id_] = i;
       return;
@@ -379,6 +380,7 @@ class Sampler {
     };
     u64 before;
     const u64 z = sums(kept, &before);
+    leave();
     const int i = find(kept, before, target_of(u, z), w0_, w1_, sh_.wsum[warp_]);
     if (i >= 0) a_.out[row_id_] = i;
   }
