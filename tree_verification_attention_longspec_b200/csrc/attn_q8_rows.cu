@@ -21,7 +21,7 @@
 // P^T comes out of S^T's accumulators by movmatrix. (mma.sync: with 8 to 16 rows tcgen05's
 // 128-row tile would be nine tenths padding, and its operands would have to be converted
 // through shared memory. The other kernel takes over above kQ8MaxRows: 65,536 tokens of 8
-// heads, 24 rows a head: 59 us here, 67 there; 48 rows: 79 here, 68 there.)
+// heads, 24 rows a head: 59 us here, 69 there; 48 rows: 79 here, 70 there.)
 //
 // A chunk's keys go round the CTA's warps in steps of 16; the warps' (m, l, O) are merged in
 // shared memory at the end and leave as the chunk's partial, which combine.cu joins.
