@@ -1392,8 +1392,10 @@ class Sampler {
         const int e = __ffs(__ballot_sync(0xffffffffu, upto >= left)) - 1;
         const uint32_t first = __shfl_sync(0xffffffffu, upto - c, e);
         const bool over = __shfl_sync(0xffffffffu, past ? 1 : 0, e);
-        found = left > first;
         bk = kKeysPer * g + e;
+        // Zeros have a bin ahead of all entries without one, but the positive ones of those come
+        // before them in the order: how many zeros are kept is not told from the counts.
+        found = left > first && !(bk == map.zero && map.pos > 0 && n_tiny > 0u);
         room = left - first;
         if (warp_ == g / 32) {  // its weight is what is kept of it
           const uint32_t kept = lane_ < e ? c : lane_ == e ? room : 0u;
