@@ -7,10 +7,11 @@
 //   a block that already holds tokens keeps its scale s where s >= unit; where s < unit its
 //   earlier codes c become the codes nearest to c * (s / unit) and its scale becomes unit;
 //   code = nearest e4m3 of x / scale (ties to even, saturated).
-// Units are powers of two, so x / unit and c * (s / unit) are exact before their one
-// rounding, and a scale that grows costs the earlier codes nothing but bits that fall
+// Units are powers of two, so x / unit and, between units, c * (s / unit) are exact before their
+// one rounding, and a scale that grows costs the earlier codes nothing but bits that fall
 // below e4m3's smallest: a block's content depends on what is in it, hardly on the calls
-// that brought it. (A tighter scale, amax / 448, gains under one bit of range and none of
+// that brought it. (Where another writer's s is none, quotient and product are rounded to odd
+// first, so that the code is still the nearest to the exact value.) (A tighter scale, amax / 448, gains under one bit of range and none of
 // precision, the codes being floating point.)
 //
 // A team of 1, 2, 4 or 8 warps per block, head and tensor, so that a lane holds at most 8
@@ -59,15 +60,38 @@ __device__ void new_lengths(const AppendArgs& a) {
   }
 }
 
-// Eight bf16 values times (or, `divide`, over) s as codes.
-__device__ __forceinline__ uint2 encode(const uint4& v, float s, bool divide) {
+// Eight bf16 values times a power of two as codes (the products are exact).
+__device__ __forceinline__ uint2 encode(const uint4& v, float s) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float x = __uint_as_float(w[k] << 16), y = __uint_as_float(w[k] & 0xffff0000u);
-    c[k] = divide ? f32x2_e4m3x2(__fdiv_rn(x, s), __fdiv_rn(y, s)) : f32x2_e4m3x2(x * s, y * s);
-  }
+  for (int k = 0; k < 4; ++k)
+    c[k] = f32x2_e4m3x2(__uint_as_float(w[k] << 16) * s, __uint_as_float(w[k] & 0xffff0000u) * s);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// Quotients and products that fp32 does not hold are rounded to odd (towards zero, then the
+// last bit set): 24 bits of which the last says that there is more are rounded to a code's 4
+// as the exact value would be, where fp32's nearest could land on the middle of two codes.
+__device__ __forceinline__ float to_odd(float towards_zero, float rest) {
+  return rest > 0.f || rest < 0.f ? __uint_as_float(__float_as_uint(towards_zero) | 1u) : towards_zero;  // (NaN, infinity: as they are)
+}
+__device__ __forceinline__ float quotient(float x, float s) {
+  const float q = __fdiv_rz(x, s);
+  return to_odd(q, fmaf(-q, s, x));
+}
+__device__ __forceinline__ float product(float x, float s) {
+  const float q = __fmul_rz(x, s);
+  return to_odd(q, fmaf(x, s, -q));
+}
+
+// Eight bf16 values over s as codes.
+__device__ __forceinline__ uint2 encode_over(const uint4& v, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    c[k] = f32x2_e4m3x2(quotient(__uint_as_float(w[k] << 16), s), quotient(__uint_as_float(w[k] & 0xffff0000u), s));
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
@@ -196,8 +220,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q8_append_kernel(const __grid_
         const uint32_t lo = e4m3x2_f16x2(cw[k]), hi = e4m3x2_f16x2_hi(cw[k]);
         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        cw[k] = (uint32_t)f32x2_e4m3x2(x.x * ratio, x.y * ratio) |
-                ((uint32_t)f32x2_e4m3x2(y.x * ratio, y.y * ratio) << 16);
+        cw[k] = (uint32_t)f32x2_e4m3x2(product(x.x, ratio), product(x.y, ratio)) |
+                ((uint32_t)f32x2_e4m3x2(product(y.x, ratio), product(y.y, ratio)) << 16);
       }
       *at = c;
     }
@@ -210,14 +234,14 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q8_append_kernel(const __grid_
     const float inv = 1.f / now;
 #pragma unroll
     for (int s = 0; s < kKeep; ++s)
-      if (there >> s & 1u) store(s, encode(keep[s], inv, false));
+      if (there >> s & 1u) store(s, encode(keep[s], inv));
   } else {
     // another writer's scale, kept: divisions, in a loop of their own (unrolled with the rest
     // they were most of the kernel's code, and its time)
 #pragma unroll 1
     for (int s = 0; s < kKeep; ++s) {
       const int r = source(i0 + s * kRows);
-      if (r >= 0) store(s, encode(fetch(r), now, true));
+      if (r >= 0) store(s, encode_over(fetch(r), now));
     }
   }
 }
