@@ -380,8 +380,19 @@ typedef struct {
  * values as ls_kv_q8 describes them. q, k_tree and v_tree are bf16 as there; tree_size = 1
  * is a decoding step whose token is not in the cache yet. Tree values must be finite and
  * below 2^78 in magnitude. Workspace: ls_verify_attn_q8_workspace_size(dims, tree) bytes.
- * The weights enter the product with the values rounded to f16 (relative 2^-11); scores and
- * sums are fp32. ls_verify_attn_check reads the device status.
+ * ls_verify_attn_check reads the device status.
+ *
+ * Accuracy. Scores, their maxima and the sums of weights are fp32. A weight w (of a row) and
+ * its key's value scale s are multiplied with the code as one number rounded to f16: with M
+ * the row's largest w * s, it is off by at most max(2^-11 w s, 2^-34 M). That is 2^-11 for
+ * every key whose w * s is at least 2^-23 M. Below that, keys lose bits that show only in
+ * dimensions where the keys that weigh most hold zeros: at equal weights, in blocks whose
+ * value scale is more than 2^23 below another block's (2^34 below, they count for nothing
+ * there). lse is not concerned, down to w * s = 2^-135 M. A tree node's s is a power of two
+ * between 2^-15 and 2^-14 of the largest |v| of its tree (or of 16 nodes of it), at least
+ * 2^-60. q's rows and the tree's keys and values are multiplied as f16 numbers of that kind:
+ * exact but for elements below 2^-31 of the largest (of the row, or of the tree and head),
+ * which are off by at most 2^-39 of it.
  */
 LS_API size_t ls_verify_attn_q8_workspace_size(const ls_verify_dims* dims, const ls_tree_opts* tree);
 LS_API int ls_verify_attn_q8(const void* q, const ls_kv_q8* kv, const void* k_tree, const void* v_tree,

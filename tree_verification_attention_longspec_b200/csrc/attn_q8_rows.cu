@@ -8,7 +8,10 @@
 //   O += p_j vc_j,   l += p_j / vs_j
 // m is the running maximum of x_j + log2 vs_j (raised only when exceeded by kRaise), so p_j
 // lies in f16's range, p and the codes are f16 operands (the codes exactly) and the scales
-// cost one FMA a score. out = O / l, lse = m - kOff + log2 l.
+// cost one FMA a score. out = O / l, lse = m - kOff + log2 l. As f16, p_j is off by 2^-11 of
+// itself or by 2^-25, whichever is more: w_j vs_j by max(2^-11 w_j vs_j, 2^-34 M) with M the
+// row's largest, so blocks of values far below another's (2^23 at equal weights) lose bits in
+// dimensions where the other holds zeros.
 //
 // Decoding and small trees read each cached byte for few rows: HBM bounds them, and what
 // keeps HBM busy is bytes in flight. Every warp streams its own keys, 16 at a step, through

@@ -9,13 +9,16 @@
 // f16, so K and V become f16 tiles in shared memory, Q becomes f16 in place (each row times
 // a power of two that brings its largest element to [2^14, 2^15): exact down to 2^-29 of
 // it), and so do the tree block's keys and values (a power of two for each of the two
-// tiles). P is f16 too: 11 bits where bf16 has 8.
+// tiles). P is f16 too: 11 bits where bf16 has 8, as long as it is at least 2^-14 (see Scales).
 // Scales. A score is s * ck + lv in the log2 domain, ck the key block's scale times the
 // softmax scale over the row's power of two, lv = log2 of the value scale; both are constant
 // over 16 keys (no scale block is shorter), so they cost one multiplier and one addend a
 // group. P = 2^(s * ck + lv - m + kOff) then carries the value scale, the product needs
 // none, and the row's sum takes it out again, 1 / vs a group. m is the running maximum of
-// s * ck + lv, raised when exceeded by kRaise, so P stays below 2^15.
+// s * ck + lv, raised when exceeded by kRaise, so P stays below 2^15. What this costs: a weight
+// times its scale that is below 2^-23 of the row's largest such product (M) is a subnormal f16,
+// off by up to 2^-25, which is 2^-34 M; a block of much smaller values than another's loses
+// bits to it, in dimensions where that one holds zeros.
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warps 0-3, 4-7  softmax of tile 0, of tile 1
