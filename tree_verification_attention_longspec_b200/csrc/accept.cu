@@ -21,6 +21,7 @@
 
 #include "ls_device.cuh"
 #include "ls_verify_attn.h"
+#include "tree_walk.cuh"
 
 namespace ls {
 
@@ -181,24 +182,19 @@ __global__ void __launch_bounds__(kWalkThreads) accept_walk_kernel(AcceptArgs a)
     am[tid] = bi == INT32_MAX ? 0 : bi;  // no value above -inf: index 0
   }
   __syncthreads();
-  // the smallest child of every node whose draft token is that node's argmax
-  if (ok && tid > 0 && tid < n && tok[tid] == am[par[tid]]) atomicMin(&first_match[par[tid]], tid);
+  __shared__ int32_t path[kMaxTree], len_s;
+  if (ok) {  // the same for the whole CTA
+    const int len = walk_tree(am, par, tok, first_match, n, path);
+    if (tid == 0) len_s = len;
+  } else if (tid == 0) {
+    len_s = -1;
+  }
   __syncthreads();
+  const int len = len_s;
+  if (tid <= len) a.accept_path[(int64_t)b * a.T + tid] = path[tid];
   if (tid == 0) {
-    int32_t* path = a.accept_path + (int64_t)b * a.T;
-    if (!ok) {
-      a.accept_len[b] = -1;
-      a.next_token[b] = -1;
-    } else {
-      int cur = 0, len = 0;
-      path[0] = 0;
-      while (first_match[cur] < n) {  // children lie above their parent: the walk ends
-        cur = first_match[cur];
-        path[++len] = cur;
-      }
-      a.accept_len[b] = len;
-      a.next_token[b] = am[cur];
-    }
+    a.accept_len[b] = len;
+    a.next_token[b] = ok ? am[path[len]] : -1;
   }
 }
 

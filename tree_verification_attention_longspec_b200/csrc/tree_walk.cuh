@@ -1,4 +1,5 @@
-// The walk down a verified draft tree, given the target's token at every node.
+// The walk down a verified draft tree, given the target's token at every node (its argmax, or
+// the token drawn there): the one rule of both acceptance calls.
 #pragma once
 #include "ls_device.cuh"
 
