@@ -14,6 +14,7 @@
 namespace {
 
 using ls::Plan;
+using ls::device_info;
 
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultWaitNs = 4000000000ull;  // 4 s
@@ -21,7 +22,9 @@ constexpr uint64_t kMaxWaitNs = 60000000000ull;     // 60 s
 int g_sm_count[kMaxDevices];  // 0 = not queried yet; a benign race writes the same value
 int g_cc_major[kMaxDevices];
 
-int device_info(int* sm_count, int* cc_major) {
+}  // namespace
+
+int ls::device_info(int* sm_count, int* cc_major) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return LS_ERR_CUDA;
   if (dev < kMaxDevices && g_sm_count[dev] > 0) {
@@ -41,6 +44,8 @@ int device_info(int* sm_count, int* cc_major) {
   *cc_major = major;
   return LS_OK;
 }
+
+namespace {
 
 int check_dims(const ls_verify_dims* d) {
   if (d == nullptr) return LS_ERR_INVALID_ARG;

@@ -96,6 +96,8 @@ cudaError_t configure_once(Kernel kernel, int smem, bool (&configured)[kMaxConfi
 
 // Launchers (defined in the kernel files, called by the host API).
 namespace ls {
+// The current device's SMs and compute capability, asked for once a device (in api.cu); a status.
+int device_info(int* sm_count, int* cc_major);
 cudaError_t launch_partials(const PartialsArgs& a, int64_t kv_rows, cudaStream_t stream);  // kv_rows: rows of the K/V tensors
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_rope(const TreeRopeArgs& a, cudaStream_t stream);

@@ -41,10 +41,9 @@
 // 534 rows of 128,256 with it 168 us, 8 rows of 32,000 fp32 21 us.
 #include <cooperative_groups.h>
 
-#include <algorithm>
-
 #include "ls_device.cuh"
 #include "ls_verify_attn.h"
+#include "sample_plan.cuh"
 #include "tree_walk.cuh"
 
 namespace ls {
@@ -73,14 +72,11 @@ constexpr int kFine = 4096;      // bins of the first histogram
 constexpr int kFinePer = kFine / kThreads;
 constexpr int kFineUnit = 128;   // of them for one unit of x, where x spans the weights' whole range
 constexpr int kList = 1024;      // entries of the border bins kept aside, two per thread
-constexpr int kMaxCluster = 8;
-constexpr int kPlaces = 2 * 148;  // CTAs that run at once: two on each SM of a B200
 constexpr int kMaxVocab = 1 << 20;  // sums of 2^43 stay below 2^63
 constexpr int kWeightBits = 43;
 constexpr float kMaxX = 30.6f;  // exp(-30.6) is below half a unit
-// a weight's three parts: a CTA's share is at most 2^17 entries, so their sums fit 32 bits
+// a weight's three parts: a CTA's share is at most kMaxSeg entries, so their sums fit 32 bits
 constexpr int kPartBits = 15;
-constexpr int kMaxSeg = 1 << 17;
 constexpr int kLut = 1024;  // e^(-b / 32) * 2^43
 constexpr int kKeys = 4096;  // bins of the histogram over bf16 values
 constexpr int kKeysPer = kKeys / kThreads;  // of a group; the cluster has a group for each thread of a CTA
@@ -1902,13 +1898,12 @@ int run_sample(const void* logits, int64_t row_stride, const float* uniform, con
   a.V = vocab;
   a.cap = cap;
   a.vec = (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 && (row_stride * elt) % 16 == 0 ? 1 : 0;
-  // the fewest CTAs whose shared memory holds the row; more while the rows leave places idle
-  // and a CTA's share is worth its part in the exchanges (8 rows of 32,000 fp32: 22.7 us with
-  // 8 CTAs a row, 24 with 4, 26 with 2; 32 rows of them: 30.7 with 8, 26.6 with 4)
-  int cluster = 1;
-  while (cluster < kMaxCluster && (vocab + cluster - 1) / cluster > std::min(cap, kMaxSeg) - 8) cluster *= 2;
-  while (cluster < kMaxCluster && rows * cluster * 2 <= kPlaces && vocab / cluster >= 4096) cluster *= 2;
-  a.seg = ((vocab + cluster - 1) / cluster + 7) / 8 * 8;
+  int sms = 0, major = 0;
+  const int rd = device_info(&sms, &major);
+  if (rd != LS_OK) return rd;
+  if (major != 10) return LS_ERR_UNSUPPORTED;
+  const int cluster = sample_cluster(rows, vocab, cap, sms);
+  a.seg = sample_share(vocab, cluster);
   (void)cudaGetLastError();
   return f32 ? launch_sample<true>(a, rows, cluster, st) : launch_sample<false>(a, rows, cluster, st);
 }
