@@ -5,7 +5,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <vector>
+#include <memory>
+#include <new>
 
 #include "ls_device.cuh"
 #include "ls_verify_attn.h"
@@ -126,7 +127,9 @@ int make_plan(const ls_verify_dims* d, Plan* p, bool with_tree = true, const ls_
   q.combine_wide = out_rows < 4LL * sms ? 1 : 0;
   q.n_combine = (int32_t)(q.combine_wide ? out_rows : (out_rows + ls::kMergeRows - 1) / ls::kMergeRows);
 
-  std::vector<int32_t> blocks(q.B);
+  // (no exception leaves a C entry: a batch that the host has no memory for is refused)
+  const std::unique_ptr<int32_t[]> blocks(new (std::nothrow) int32_t[q.B]);
+  if (blocks == nullptr) return LS_ERR_UNSUPPORTED;
   int32_t max_blocks = 0;
   for (int b = 0; b < q.B; ++b) {
     const int32_t L = d->cu_seqlens_host ? d->cu_seqlens_host[b + 1] - d->cu_seqlens_host[b]
@@ -660,13 +663,16 @@ int ls_verify_attn_check(const ls_verify_dims* dims, const void* workspace, void
   if (rc != LS_OK) return rc;
   if (workspace == nullptr) return LS_ERR_WORKSPACE;
   const ls::Layout lay = ls::make_layout(p);
-  std::vector<uint32_t> st(p.n_combine);
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return LS_ERR_CUDA;
-  if (cudaMemcpy(st.data(), static_cast<const char*>(workspace) + lay.status,
-                 st.size() * sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
-    return LS_ERR_CUDA;
-  uint32_t all = 0;
-  for (uint32_t v : st) all |= v;
+  constexpr int32_t kPiece = 4096;  // words copied at once
+  uint32_t st[kPiece], all = 0;
+  for (int32_t at = 0; at < p.n_combine; at += kPiece) {
+    const int32_t n = std::min(kPiece, p.n_combine - at);
+    if (cudaMemcpy(st, static_cast<const char*>(workspace) + lay.status + (size_t)at * sizeof(uint32_t),
+                   n * sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return LS_ERR_CUDA;
+    for (int32_t i = 0; i < n; ++i) all |= st[i];
+  }
   if (all & ls::kErrLengths) return LS_ERR_LENGTHS;
   if (all & ls::kErrBadTree) return LS_ERR_BAD_TREE;
   if (all & ls::kErrTimeout) return LS_ERR_TIMEOUT;
