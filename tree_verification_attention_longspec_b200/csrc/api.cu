@@ -132,9 +132,10 @@ int make_plan(const ls_verify_dims* d, Plan* p, bool with_tree = true, const ls_
   if (blocks == nullptr) return LS_ERR_UNSUPPORTED;
   int32_t max_blocks = 0;
   for (int b = 0; b < q.B; ++b) {
-    const int32_t L = d->cu_seqlens_host ? d->cu_seqlens_host[b + 1] - d->cu_seqlens_host[b]
-                                         : d->max_prefix_len;
-    blocks[b] = ls::prefix_blocks(ls::attended_len(q, L)) + (with_tree ? 1 : 0);  // prefix blocks, tree block
+    // what the sequence attends, or without its length the most that one within the bound does
+    const int32_t keys = d->cu_seqlens_host ? ls::attended_len(q, d->cu_seqlens_host[b + 1] - d->cu_seqlens_host[b])
+                                            : ls::attended_most(q, d->max_prefix_len);
+    blocks[b] = ls::prefix_blocks(keys) + (with_tree ? 1 : 0);  // prefix blocks, tree block
     if (blocks[b] > max_blocks) max_blocks = blocks[b];
   }
   const long long units = (long long)q.Hkv * q.rg;

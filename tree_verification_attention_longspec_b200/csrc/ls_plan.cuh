@@ -107,6 +107,16 @@ LS_HD int32_t attended_len(const Plan& p, int32_t L) {
   return L - window_start(p, L);
 }
 
+// The most keys that a sequence of at most L keys may have to attend. (With a window,
+// attended_len is W - 1 plus up to 127 keys before it in their block, which a shorter
+// sequence may have more of than a longer one.)
+LS_HD int32_t attended_most(const Plan& p, int32_t L) {
+  if (L <= 0) return 0;
+  if (p.window <= 0) return L;
+  const int64_t most = (int64_t)p.window + kBlockN - 2;
+  return most < L ? (int32_t)most : L;
+}
+
 // The first attended key (index into [window_start, L)) that a row at tree depth `depth`
 // may see; 0 without a window.
 LS_HD int32_t window_cut(const Plan& p, int32_t L, int32_t depth) {
