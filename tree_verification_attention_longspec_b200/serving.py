@@ -181,7 +181,8 @@ class KVCacheQ8:
 
 class _AttnQ8:
     """What the two attention calls share: fixed dims and one workspace, any inputs of those
-    shapes. Calls of one object, captured ones included, must not overlap on the GPU."""
+    shapes. Calls of one object, captured ones included, must not overlap on the GPU, and a
+    graph that holds one needs the object for as long as it is replayed."""
 
     with_tree = True
 
@@ -204,6 +205,7 @@ class _AttnQ8:
             raise LSError(1, f"{self._name}_workspace_size returned 0 (invalid or unsupported dims)")
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
         self._ws_ptr = self.workspace.data_ptr()
+        self._home = _raw_stream(dev.index)  # the stream that the workspace was allocated on
         self._fn = getattr(load_library(), self._name)
         self._rows = batch * tree_size
         self._kind = (batch, num_kv_heads, head_dim, dev.index)
@@ -218,6 +220,9 @@ class _AttnQ8:
                 raise ValueError(f"the cache is on {cache.device}, the call on {self.device}")
             raise ValueError("the cache's batch, kv heads or head dimension are not the call's")
         dev, d = self.device, self.dims
+        if _raw_stream(dev.index) != self._home and not torch.cuda.is_current_stream_capturing():
+            # freed with this object, the memory waits for the call's stream before it is used again
+            self.workspace.record_stream(torch.cuda.current_stream(dev))
         rows = self.tree.total_nodes if self.tree is not None and self.tree.cu_tree else self._rows
         if rows != self._shapes[3][0]:
             self._shapes = self._shapes_of(rows)
