@@ -8,10 +8,10 @@ statically, so the library loads wherever the driver does.
 
 --debug builds the index-checking library, libls_verify_attn_debug.so: the same
 sources compiled with LS_DEBUG, so that every TMA coordinate and global index that the
-kernels of the bf16 caches (partials, combine, tree positions) form is checked against its
-tensor's extent and a failed check is reported by ls_verify_attn_check as LS_ERR_INDEX. It
-is a separate library with the same entry points, for tests; the product library has no
-checks. (The 8-bit cache's kernels bound every page that they look up in both libraries.)
+attention kernels (partials, 8-bit cache, combine, tree positions) form is checked against
+its tensor's extent and a failed check is reported by ls_verify_attn_check as LS_ERR_INDEX,
+and so that a bounded wait's probes return at once. It is a separate library with the same
+entry points, for tests; the product library has no checks beyond its bounds on pages.
 """
 from __future__ import annotations
 

@@ -172,10 +172,21 @@ __global__ void __launch_bounds__(32 * warps_of(NT), ctas_of(NT)) q8_rows_kernel
   const uint8_t* kbase = kv.k_pages + c.kh * D + 16 * ch + kr * stride;
   const uint8_t* vbase = kv.v_pages + c.kh * D + 16 * ch + kr * stride;
   const float* sbase = (lane ? kv.v_scale : kv.k_scale) + c.kh;
+#if defined(LS_DEBUG)
+  uint32_t dbg = 0u;
+  LS_DCHECK(dbg, (int64_t)blockIdx.x < p.n_chunks && p.slot_rows == R && c.b < p.B && c.kh < p.Hkv);
+  LS_DCHECK(dbg, tree_base >= 0 && tree_base + tree_n <= p.N && (row0 + rows - 1) / p.g < tree_n);
+  LS_DCHECK(dbg, c.key_begin == c.key_end || (c.key_begin % kStep == 0 && c.key_skip % kStep == 0));
+  LS_DCHECK(dbg, c.key_skip + c.key_end <= seq_len);
+#endif
   // cache row of the step's first key (a step never crosses a page: both are multiples of 16)
-  auto find = [&](int key) -> int32_t { return key < c.key_end ? q8_row(kv, c.b, c.key_skip + key) : 0; };
+  auto find = [&](int key) -> int32_t {
+    LS_DCHECK(dbg, key >= c.key_end || q8_page_exists(kv, c.b, c.key_skip + key));
+    return key < c.key_end ? q8_row(kv, c.b, c.key_skip + key) : 0;
+  };
   auto copy = [&](int stage, int key, int32_t row) {
     if (key < c.key_end) {
+      LS_DCHECK(dbg, row >= 0 && row + kStep <= kv.num_pages * kv.page_size && row % kStep == 0);
       const uint32_t to = ring_at + stage * Rg::kStage;
       const int64_t from = (int64_t)row * stride;
       const uint8_t *kp = kbase + from, *vp = vbase + from;
@@ -566,7 +577,11 @@ __global__ void __launch_bounds__(32 * warps_of(NT), ctas_of(NT)) q8_rows_kernel
     *reinterpret_cast<float4*>(a.o_part + (slot + r) * D + d) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (d == 0) a.lse_part[slot + r] = M == -INFINITY ? -INFINITY : M - kOff + log2f(L);
   }
-  if (tid == 0) a.chunk_status[blockIdx.x] = bad_s ? kErrBadTree : 0u;
+  uint32_t status = bad_s ? kErrBadTree : 0u;
+#if defined(LS_DEBUG)
+  status |= __syncthreads_or((int)dbg) ? kErrIndex : 0u;
+#endif
+  if (tid == 0) a.chunk_status[blockIdx.x] = status;
 }
 
 template <int D, int NT>

@@ -120,6 +120,7 @@ struct Bars {
   uint32_t tmem_base;
   uint32_t abort;
   uint32_t tree_err;                    // a parent link that is not a rooted tree's
+  uint32_t dbg;                         // index-checking builds: kErrIndex once a check failed
   int32_t mask_slot;
   float kc[kTables][kGroups];           // key scales of the block's groups
   float lv[kTables][kGroups];           // log2 of the value scales
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     bars->tree_max[0] = bars->tree_max[1] = 0u;
     bars->abort = 0u;
     bars->tree_err = 0u;
+    bars->dbg = 0u;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -414,6 +416,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     const int n_pages = (seq_len + kv.page_size - 1) / kv.page_size;
     int issued = 0, slot = 0, use = 0;
     bool ok = true;
+#if defined(LS_DEBUG)
+    // the unit's nodes lie inside the tree tensors (rows of the Q box past the last read zeros),
+    // its keys inside the sequence, its partial inside o_part
+    if (lane == 0 && !(tok0 >= 0 && tok0 < tree_n && tree_base >= 0 && tree_base + tree_n <= p.N &&
+                       c.key_skip + c.key_end <= seq_len && (int64_t)blockIdx.x < p.n_chunks && c.b < p.B && c.kh < p.Hkv))
+      bars->dbg = kErrIndex;
+#endif
     // A block's scales are read when its keys are asked for, and go into the table one block
     // later, when they have come.
     float ks = 1.f, vs = 1.f;
@@ -456,6 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
         if (lp >= kv.max_pages) lp = kv.max_pages - 1;
         const int32_t page = kv.page_table[(size_t)c.b * kv.max_pages + lp];
         prow = ((uint32_t)page < (uint32_t)kv.num_pages ? page : 0) * kv.page_size + key % kv.page_size;
+#if defined(LS_DEBUG)
+        // a box with keys of the sequence is a page's of the cache, and any box lies inside it
+        if ((key < c.key_skip + c.key_end && !q8_page_exists(kv, c.b, key)) || prow < 0 ||
+            prow + bh > kv.num_pages * kv.page_size)
+          bars->dbg = kErrIndex;
+#endif
       }
       if (!val) {
         put_scales();
@@ -1003,7 +1018,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     tc_fence_after_sync();
     tmem_dealloc(tbase, C::kTmemCols);
   }
-  if (tid == 0) a.chunk_status[blockIdx.x] = (bars->abort ? kErrTimeout : 0u) | (bars->tree_err ? kErrBadTree : 0u);
+  if (tid == 0)
+    a.chunk_status[blockIdx.x] = (bars->abort ? kErrTimeout : 0u) | (bars->tree_err ? kErrBadTree : 0u) | bars->dbg;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

@@ -37,6 +37,14 @@ __device__ __forceinline__ int32_t q8_row(const KvQ8& kv, int32_t b, int32_t key
   return ((uint32_t)page < (uint32_t)kv.num_pages ? page : 0) * kv.page_size + in;
 }
 
+#if defined(LS_DEBUG)
+// Whether the table names a page of the cache for key `key` of sequence b.
+__device__ __forceinline__ bool q8_page_exists(const KvQ8& kv, int32_t b, int32_t key) {
+  const int32_t lp = key / kv.page_size;
+  return lp < kv.max_pages && (uint32_t)kv.page_table[(size_t)b * kv.max_pages + lp] < (uint32_t)kv.num_pages;
+}
+#endif
+
 // Two e4m3 codes (low 16 bits of w) as packed f16: exact, NaN codes stay NaN.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
   uint32_t r;

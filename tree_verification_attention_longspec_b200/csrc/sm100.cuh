@@ -38,11 +38,17 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                : "memory");
 }
 
+#if defined(LS_DEBUG)
+#define LS_MBAR_PROBE "mbarrier.test_wait"  // returns at once
+#else
+#define LS_MBAR_PROBE "mbarrier.try_wait"  // may suspend the thread for a while of the hardware's choosing
+#endif
+
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      LS_MBAR_PROBE ".parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -54,7 +60,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // `timeout_ns` of global time, or as soon as another thread has raised *abort, and
 // then returns false (raising *abort itself on a timeout). Never spins forever: each
 // probe that the barrier does not complete returns after a time limit of the hardware's,
-// and the loop checks the clock between probes.
+// and the loop checks the clock between probes. (The index-checking build's probes return at
+// once, so that there a limit of a nanosecond runs out wherever a wait waits at all.)
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
                                                   volatile uint32_t* abort, uint64_t timeout_ns) {
   if (mbar_try_wait(bar, parity)) return true;
