@@ -42,10 +42,9 @@
 // Every wait is bounded (the call's wait limit, 4 s by default): on a timeout the CTA
 // raises an abort flag, all roles drain their in-flight copies and MMAs, TMEM is freed,
 // and the chunk status reports it.
-#include <cudaTypedefs.h>
-
 #include "ls_device.cuh"
 #include "sm100.cuh"
+#include "tensor_maps.cuh"
 
 namespace ls {
 namespace {
@@ -57,9 +56,6 @@ constexpr int kMmaWarp = 9;
 constexpr int kMaxSlots = 12;
 constexpr int kTiles = 2;  // 128-row query tiles per CTA
 constexpr int kHalf = 64;  // keys per P half
-// Draining after an abort waits for copies and MMAs that were issued and always
-// complete; its own bound is fixed (the call's wait limit may be far shorter).
-constexpr uint64_t kDrainNs = 4000000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 static_assert(kUnitRows == kTiles * 128, "a unit is two 128-row tiles");
 
@@ -114,26 +110,6 @@ constexpr int smem_need() {
   return Cfg<D>::kBarOff + (int)sizeof(Bars) + 1024;
 }
 static_assert(smem_need<128>() <= kSmemWindow && smem_need<64>() <= kSmemWindow, "shared memory");
-
-// AND of `pred` over the `n` threads that meet at named barrier `id`.
-__device__ __forceinline__ bool bar_and(uint32_t id, uint32_t n, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(pred ? 1u : 0u), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-
-// Waits only on time (used to drain in-flight work after an abort).
-__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t never = 0;
-  return mbar_wait_bounded(bar, parity, &never, kDrainNs);
-}
 
 // P = 2^(s*cs - m) for 64 scores, packed to bf16 pairs; adds the values to (sum0, sum1)
 // and their bf16 roundings, the weights the PV product uses, to (rsum0, rsum1). The
@@ -813,18 +789,6 @@ __global__ void __launch_bounds__(kThreads, 1) partials_tc_kernel(const __grid_c
     a.chunk_status[blockIdx.x] = (bars->abort ? kErrTimeout : 0u) | (bars->tree_err ? kErrBadTree : 0u) | bars->dbg;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (fn == nullptr) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 // K or V cache viewed as [rows][H_kv][D] bf16; boxes of 128 rows x 64 elements of one head.
 bool make_kv_map(CUtensorMap* map, const void* base, int D, int Hkv, int64_t rows, int box_rows = 128) {
   auto fn = encode_fn();
@@ -834,36 +798,6 @@ bool make_kv_map(CUtensorMap* map, const void* base, int D, int Hkv, int64_t row
   cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// Q viewed as [B*T nodes][H_kv][g][D] bf16; a box is 64 elements x g heads x one kv
-// head x tpu nodes, which lands as tpu*g consecutive 128-byte rows, node-major.
-bool make_q_map(CUtensorMap* map, const void* base, int D, const Plan& p) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.g, (cuuint64_t)p.Hkv, (cuuint64_t)(p.N > 0 ? p.N : 1)};
-  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.g * D * 2, (cuuint64_t)p.Hq * D * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)p.g, 1, (cuuint32_t)p.tpu};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// o_part viewed as [n_chunks * 256 rows][D] fp32; boxes of 128 rows x 32 floats (128 B),
-// 128B-swizzled like the kernel's staging.
-bool make_o_map(CUtensorMap* map, float* base, int D, int64_t rows) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)(rows > 0 ? rows : 1)};
-  cuuint64_t strides[1] = {(cuuint64_t)D * 4};
-  cuuint32_t box[2] = {32, 128};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;

@@ -1,4 +1,4 @@
-// Thin inline-PTX wrappers for the sm_100a features the prefix kernel uses:
+// Thin inline-PTX wrappers for the sm_100a features the tensor-core kernels use:
 // mbarriers, TMA tensor loads, tensor memory (TMEM) allocation/load/store, UMMA
 // shared-memory and instruction descriptors, and tcgen05.mma / tcgen05.commit.
 // Written from the PTX ISA's descriptions of these instructions.
@@ -74,6 +74,29 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
       return false;
     }
   }
+}
+
+// Draining after an abort waits for copies and MMAs that were issued and always
+// complete; its own bound is fixed (the call's wait limit may be far shorter).
+constexpr uint64_t kDrainNs = 4000000000ull;
+// Waits only on time (used to drain in-flight work after an abort).
+__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t never = 0;
+  return mbar_wait_bounded(bar, parity, &never, kDrainNs);
+}
+
+// AND of `pred` over the `n` threads that meet at named barrier `id`.
+__device__ __forceinline__ bool bar_and(uint32_t id, uint32_t n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
 }
 
 // Makes generic-proxy writes to shared memory visible to the async proxy (TMA, UMMA).
