@@ -1,7 +1,8 @@
 """The 8-bit paged cache, attention over it, and sampling, in fp64 — TEST INFRASTRUCTURE ONLY.
 
-Only ``tests/`` may import this module; the CUDA path never does and shares no code with
-it. Written as plain loops over sequences, blocks and rows from the definitions:
+Only ``tests/`` and the smoke check may import this module; the CUDA path never does and
+shares no code with it. Written as plain loops over sequences, blocks and rows from the
+definitions:
 
 - e4m3: sign, 4 exponent bits (bias 7), 3 fraction bits; exponent 0 is subnormal (steps of
   2^-9); 0x7f and 0xff are NaN, there is no infinity, the largest value is 448.
