@@ -202,8 +202,9 @@ def code_lines(text):
     return "\n".join(out)
 
 
-# Sources that hold no code of the partials kernel, of its plan or of its launch.
-OTHER_KERNELS = ("accept.cu", "attn_q8_rows.cu", "attn_q8_tc.cu", "combine.cu", "no_alloc.cu", "q8_append.cu",
+# Sources that hold no code of the partials kernel (the host API's part in its traffic, the
+# plan, is compared itself).
+OTHER_KERNELS = ("accept.cu", "api.cu", "attn_q8_rows.cu", "attn_q8_tc.cu", "combine.cu", "no_alloc.cu", "q8_append.cu",
                  "q8_device.cuh", "sample.cu", "sample_plan.cuh", "tree_rope.cu", "tree_walk.cuh")
 
 
@@ -218,15 +219,15 @@ def kernel_source_hash():
     return h.hexdigest()[:16]
 
 
-def recorded_traffic(workload_name):
+def recorded_traffic(workload_name, plan=None):
     """DRAM bytes per launch of the partials kernel from the committed ncu summary, when it
-    was taken on the current kernel sources; else None."""
+    was taken on the current kernel sources (and with this plan, where one is given); else None."""
     path = os.path.join(ROOT, "profiles", "traffic.json")
     try:
         with open(path) as f:
             rec = json.load(f)
         r = rec.get(workload_name)
-        if r and r.get("source_hash") == kernel_source_hash():
+        if r and r.get("source_hash") == kernel_source_hash() and plan in (None, r.get("plan")):
             return r.get("dram_bytes_per_launch")
     except Exception:
         pass
@@ -630,7 +631,7 @@ def run_ours(args):
         roof = {"bound": "hbm", "achieved": fig["partials_bytes"] / part_s / 1e9, "peak": hbm,
                 "unit": "GB/s"}
     roof["frac"] = roof["achieved"] / roof["peak"]
-    roof["traffic"] = recorded_traffic(w.name)
+    roof["traffic"] = recorded_traffic(w.name, op.plan)
     roof["kernel"] = "partials (ls_verify_attn_partials: prefix and tree blocks)"
     roof["peak_source"] = f"{peak_kind} (MEASURED_PEAKS.json burst)" if peak_kind == "measured" else "fallback"
     roof["kernel_us"] = partials_avg_ms * 1000.0

@@ -42,3 +42,9 @@ def test_the_headline_has_its_traffic():
     """Fails once the kernel's own sources changed: capture it again and record it in
     profiles/traffic.json, with bench.kernel_source_hash()."""
     assert bench.recorded_traffic(bench.HEADLINE.name) is not None
+
+
+def test_another_plan_has_no_record():
+    plan = {"partials_ctas": 144, "blocks_per_chunk": 29, "combine_ctas": 448}
+    assert bench.recorded_traffic(bench.HEADLINE.name, plan) is not None
+    assert bench.recorded_traffic(bench.HEADLINE.name, {**plan, "blocks_per_chunk": 30}) is None
