@@ -205,7 +205,7 @@ def code_lines(text):
 # Sources that hold no code of the partials kernel (the host API's part in its traffic, the
 # plan, is compared itself).
 OTHER_KERNELS = ("accept.cu", "api.cu", "attn_q8_rows.cu", "attn_q8_tc.cu", "combine.cu", "no_alloc.cu", "q8_append.cu",
-                 "q8_device.cuh", "sample.cu", "sample_plan.cuh", "tree_rope.cu", "tree_walk.cuh")
+                 "q8_device.cuh", "q8_pages.cuh", "sample.cu", "sample_plan.cuh", "tree_rope.cu", "tree_walk.cuh")
 
 
 def kernel_source_hash():

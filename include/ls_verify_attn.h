@@ -354,7 +354,7 @@ LS_API int ls_tree_accept_greedy(const void* logits, const int32_t* tree_tokens,
  *
  *   page_size, max_pages_per_seq, num_pages, page_table   as in ls_paged_kv; an entry
  *                  outside [0, num_pages) reads another page, or drops the rows of a write.
- *                  max_pages_per_seq * page_size < 2^31.
+ *                  max_pages_per_seq * page_size at most 2^31 - 2^21 (else LS_ERR_UNSUPPORTED).
  *   scale_block    16, 32, 64 or 128, dividing page_size (else LS_ERR_UNSUPPORTED, or
  *                  LS_ERR_INVALID_ARG where it does not divide)
  *   k_pages, v_pages   [num_pages * page_size, H_kv, d] bytes, 16-byte aligned

@@ -391,7 +391,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
     // a box is bh rows (a page, or 128 rows of a larger one); lane l issues box l of a block
     const int bh = kv.page_size < kBlockN ? kv.page_size : kBlockN;
     const int n_boxes = kBlockN / bh;
-    const int n_pages = (seq_len + kv.page_size - 1) / kv.page_size;
     int issued = 0, slot = 0, use = 0;
     bool ok = true;
 #if defined(LS_DEBUG)
@@ -433,16 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_tc_kernel(const __grid_constan
       int j, val;
       tile_of(ld, &j, &val);
       if (j == nb) continue;  // the tree block comes through the converters
-      // this lane's page box; a table entry is only a TMA coordinate, so a bad one reads zeros
-      // or another page; boxes past the sequence end read its last page (made zeros later)
+      // this lane's page box; boxes past the sequence's end read some page (made zeros later)
       int prow = 0;
       if (lane < n_boxes) {
         const int key = c.key_skip + c.key_begin + j * kBlockN + lane * bh;
-        int lp = key / kv.page_size;
-        if (lp >= n_pages) lp = n_pages - 1;
-        if (lp >= kv.max_pages) lp = kv.max_pages - 1;
-        const int32_t page = kv.page_table[(size_t)c.b * kv.max_pages + lp];
-        prow = ((uint32_t)page < (uint32_t)kv.num_pages ? page : 0) * kv.page_size + key % kv.page_size;
+        prow = q8_row(kv, c.b, key);
 #if defined(LS_DEBUG)
         // a box with keys of the sequence is a page's of the cache, and any box lies inside it
         if ((key < c.key_skip + c.key_end && !q8_page_exists(kv, c.b, key)) || prow < 0 ||

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "ls_device.cuh"
+#include "q8_pages.cuh"
 
 namespace ls {
 
@@ -16,26 +17,6 @@ constexpr int kMinScaleExp = -60, kMaxScaleExp = 64;
 
 // Query rows of a kv head up to which the 8-bit cache streams through registers (attn_q8_rows.cu).
 constexpr int kQ8MaxRows = 32;
-
-struct KvQ8 {
-  uint8_t* k_pages;  // [num_pages * page_size][Hkv][d]
-  uint8_t* v_pages;
-  float* k_scale;  // [num_pages * page_size / scale_block][Hkv]
-  float* v_scale;
-  const int32_t* page_table;  // [B][max_pages]
-  int32_t page_size, scale_block, max_pages, num_pages;
-  int32_t page_shift, scale_shift;  // their log2 (page_shift -1 where the page is no power of two)
-};
-
-// First row of the page that holds key `key` of sequence b, plus the key's place in it. A
-// table entry outside the cache reads page 0 instead (no fault, the result is unspecified).
-__device__ __forceinline__ int32_t q8_row(const KvQ8& kv, int32_t b, int32_t key) {
-  int32_t lp = kv.page_shift >= 0 ? key >> kv.page_shift : key / kv.page_size;
-  const int32_t in = key - lp * kv.page_size;
-  if (lp >= kv.max_pages) lp = kv.max_pages - 1;
-  const int32_t page = kv.page_table[(size_t)b * kv.max_pages + lp];
-  return ((uint32_t)page < (uint32_t)kv.num_pages ? page : 0) * kv.page_size + in;
-}
 
 #if defined(LS_DEBUG)
 // Whether the table names a page of the cache for key `key` of sequence b.
@@ -86,7 +67,8 @@ __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_u
 
 // The f16 forms of bf16 rows are their values times 2^shift with the row's largest
 // magnitude in [2^14, 2^15): bf16's 8 significant bits fit f16's 11, and what falls below
-// f16's subnormals is 2^-38 of the largest. shift is at most 126 and at least -113.
+// f16's subnormals is 2^-38 of the largest. shift is at most 126 and at least -113 (-114 where
+// the largest is infinite).
 __device__ __forceinline__ int f16_shift(float amax) { return min(126, 14 - exponent_of(amax)); }
 
 // Attention over the 8-bit cache.
