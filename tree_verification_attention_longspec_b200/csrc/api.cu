@@ -436,9 +436,9 @@ namespace {
 // ---- the 8-bit cache
 
 // The kernel for a kv head's rows: up to 32 stream through registers, in units of 8 or 16
-// rows (two units read the cache twice, the second time from L2 mostly: 24 rows over 64k
-// tokens of 8 heads 59 us, in the tensor cores' 128-row tiles 69); more go to those tiles (0;
-// 48 rows: 79 against 70 us).
+// rows (two units read the cache twice, the second time from L2 mostly: 32 rows over 64k
+// tokens of 8 heads 60 us, in the tensor cores' 128-row tiles 73; over 8k 23.6 and 25.6); more
+// go to those tiles (0; 48 rows over 64k: 81 against 73 us, over 8k 25.6 either way).
 int32_t q8_slot_rows(const ls_verify_dims* d) {
   if (d == nullptr || d->num_kv_heads < 1) return 8;  // make_plan refuses it
   const long long rows = (long long)d->tree_size * (d->num_q_heads / d->num_kv_heads);

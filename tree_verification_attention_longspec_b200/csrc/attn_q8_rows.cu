@@ -23,8 +23,9 @@
 // of each of its two keys, 16 of each of its four values (byte pairs of two keys by PRMT).
 // P^T comes out of S^T's accumulators by movmatrix. (mma.sync: with 8 to 16 rows tcgen05's
 // 128-row tile would be nine tenths padding, and its operands would have to be converted
-// through shared memory. The other kernel takes over above kQ8MaxRows: 65,536 tokens of 8
-// heads, 24 rows a head: 59 us here, 69 there; 48 rows: 79 here, 70 there.)
+// through shared memory. The other kernel takes over above kQ8MaxRows. 32 rows a head here and
+// there: 65,536 tokens of 8 heads 60 and 73 us, 8,192 tokens 23.6 and 25.6, 1,024 tokens 17.4
+// and 21.5; 48 rows: 81 and 73, 25.6 and 25.6, 17.4 and 21.5.)
 //
 // A chunk's keys go round the CTA's warps in steps of 16; the warps' (m, l, O) are merged in
 // shared memory at the end and leave as the chunk's partial, which combine.cu joins.

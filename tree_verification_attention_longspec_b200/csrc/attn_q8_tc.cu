@@ -43,8 +43,9 @@
 // converters run a block ahead; the raw ring gets what is left (three and four: 82.5 us, four
 // and two: 80.9).
 //
-// Measured (B200): 64 nodes, 28 heads over 4, 65,536 tokens: 81 us for both launches of the
-// call, 740 TFLOP/s, 0.45 of the measured bf16 rate; 64 nodes over 16,384 tokens: 37 us. A
+// Measured (B200): 64 nodes, 28 heads over 4, 65,536 tokens: 77 us on the device (85 a call
+// with the combine), 780 TFLOP/s, 0.47 of the measured bf16 rate; 64 nodes over 16,384 tokens:
+// 32 us (37 a call). A
 // half takes a softmax warp some 1,700 cycles, in which its SM quarter's two warps issue twice
 // 430 instructions and 64 exponentials a row (1,024 cycles of the MUFU), and two quarters a
 // converter's 350 (there being no 8-bit operand for K without Q and P in 8 bits too). Tried,

@@ -11,7 +11,7 @@ One verification step of a served model, with a cache that stays on the device::
     cu = cache.append(k_prompt, v_prompt, cu, cu_new, max_new)            # the prompts
     attend = VerifyAttnQ8(B, H_q, H_kv, d, T, max_prefix_len=longest)
     out, lse = attend(q, cache, k_tree, v_tree, parent, cu)               # each layer
-    tokens, n, path, after = tree_accept_sample(logits, u, draft, parent, T, temperature=t)
+    tokens, n, path, after = tree_accept_sample(logits, u, draft, parent, T, temperature=t)  # t: a tensor
     cu = cache.commit(k_tree, v_tree, cu, n, path)                        # what was accepted
 """
 from __future__ import annotations
@@ -330,9 +330,10 @@ def _sampling(logits, uniform, temperature, top_k, top_p, min_p, dense: bool):
 
 def sample(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
     """One token for each row of logits (bf16 or fp32 [rows, vocab], rows may be strided) from
-    uniform fp32 [rows] in [0, 1). temperature, top_k, top_p, min_p: a number for all rows, a
-    tensor with one per row (fp32; top_k int32), or None (1, off, off, off); temperature 0 is
-    greedy. The order of the filters and the draw are those of ``ls_sample``. Returns int32
+    uniform fp32 [rows] in [0, 1). temperature, top_k, top_p, min_p: a tensor with one value per
+    row (fp32; top_k int32), a number for all rows (a tensor is filled with it each call, which
+    costs a launch: keep a tensor where calls are small), or None (1, off, off, off); temperature
+    0 is greedy. The order of the filters and the draw are those of ``ls_sample``. Returns int32
     [rows]."""
     rows, vocab, stride, u, kind, opts, keep = _sampling(logits, uniform, temperature, top_k, top_p, min_p, False)
     dev = logits.device
