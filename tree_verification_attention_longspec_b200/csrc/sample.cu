@@ -354,7 +354,7 @@ class Sampler {
     const uint32_t least = least_key(a_.min_p != nullptr ? a_.min_p[row_id_] : 0.0f, t);
     const float u = a_.uniform[row_id_];
     if constexpr (!F32) {
-      if (cuts) {
+      if (cuts && !wide()) {
         KeyMap map;
         if (counted) {
           if (plain_map(t, &map) && resolve_keys(map, k, p, least, u)) return;
@@ -367,7 +367,7 @@ class Sampler {
       }
       cl_.sync();  // the memory changes hands
     }
-    if (resolve(k, p, least, u)) return;
+    if (!wide() && resolve(k, p, least, u)) return;
     cl_.sync();  // the memory changes hands
     Keep keep{0u, 0xffffffffu};
     if (k > 0) keep = select<false>(keep, top_ - low_, (u64)k, 0.0);
@@ -417,8 +417,17 @@ class Sampler {
     const float xf = (top_ - l) * inv_f_;
     return xf < kMaxX ? (u64)weight_in(l, xf) : 0ull;
   }
-  // The same for the rows that `resolve` leaves to `select`: top_ may be +inf.
-  __device__ __forceinline__ u64 weight_any(float l) const { return l == top_ ? 1ull << kWeightBits : weight(l); }
+  // The same for the rows that `resolve` leaves to `select`: top_ may be +inf, and x may not come
+  // out of fp32 (`wide`).
+  __device__ __forceinline__ u64 weight_any(float l) const {
+    if (l == top_) return 1ull << kWeightBits;
+    if (!wide()) return weight(l);
+    const float xf = (float)((top_d_ - (double)l) * inv_t_);
+    return xf < kMaxX ? (u64)weight_in(l, xf) : 0ull;
+  }
+  // Temperatures above 10^36, under which logits 2^128 apart are less than kMaxX units apart, and
+  // those below 2^-128, whose reciprocals pass fp32.
+  __device__ __forceinline__ bool wide() const { return inv_f_ < 1e-36f || inv_f_ == INFINITY; }
 
   __device__ __forceinline__ static u64 target_of(float u, u64 z) {
     const double at = u > 0.f ? (double)u * (double)z : 0.0;
