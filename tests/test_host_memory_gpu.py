@@ -45,13 +45,13 @@ def test_a_batch_without_host_memory_is_refused():
 def test_the_status_of_many_combine_ctas_is_read_whole():
     """Words past the first piece that the check copies count too."""
     from tree_verification_attention_longspec_b200 import binding
-    B, T, H = 700, 8, 8  # 11,200 CTAs of the combine kernel
+    B, T, H = 700, 64, 8  # 89,600 CTAs of the combine kernel
     dims = binding.make_dims(B, H, H, 64, T, max_prefix_len=16)[0]
     ws = torch.zeros(binding.workspace_size(dims), dtype=torch.uint8, device="cuda")
     stream = torch.cuda.current_stream().cuda_stream
     words = ws.view(torch.int32)
     n = B * T * H // 4
-    for at, code, want in ((0, 1, 5), (4095, 4, 6), (4096, 2, 7), (n - 1, 1, 5)):
+    for at, code, want in ((0, 1, 5), (65535, 4, 6), (65536, 2, 7), (n - 1, 1, 5)):
         words.zero_()
         assert binding.check(dims, ws.data_ptr(), stream) == 0
         words[at] = code

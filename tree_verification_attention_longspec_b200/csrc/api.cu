@@ -666,11 +666,13 @@ int ls_verify_attn_check(const ls_verify_dims* dims, const void* workspace, void
   if (workspace == nullptr) return LS_ERR_WORKSPACE;
   const ls::Layout lay = ls::make_layout(p);
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return LS_ERR_CUDA;
-  constexpr int32_t kPiece = 4096;  // words copied at once
-  uint32_t st[kPiece], all = 0;
-  for (int32_t at = 0; at < p.n_combine; at += kPiece) {
-    const int32_t n = std::min(kPiece, p.n_combine - at);
-    if (cudaMemcpy(st, static_cast<const char*>(workspace) + lay.status + (size_t)at * sizeof(uint32_t),
+  const int32_t piece = std::min(p.n_combine, 1 << 16);  // words copied at once
+  const std::unique_ptr<uint32_t[]> st(new (std::nothrow) uint32_t[piece]);
+  if (st == nullptr) return LS_ERR_UNSUPPORTED;
+  uint32_t all = 0;
+  for (int32_t at = 0; at < p.n_combine; at += piece) {
+    const int32_t n = std::min(piece, p.n_combine - at);
+    if (cudaMemcpy(st.get(), static_cast<const char*>(workspace) + lay.status + (size_t)at * sizeof(uint32_t),
                    n * sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
       return LS_ERR_CUDA;
     for (int32_t i = 0; i < n; ++i) all |= st[i];
