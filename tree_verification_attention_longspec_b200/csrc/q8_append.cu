@@ -17,7 +17,7 @@
 // A team of 1, 2, 4 or 8 warps per block, head and tensor, so that a lane holds at most 8
 // loads of 8 values: all are in flight at once, give amax, and are rounded from registers.
 // Bytes bound it: each row is read once and its codes written once. Measured (B200): 16,384
-// new rows of 8 heads, 101 MB: 24 us, 4.2 TB/s (16 loads a lane and half the warps an SM:
+// new rows of 8 heads, 101 MB: 23 us, 4.4 TB/s (16 loads a lane and half the warps an SM:
 // 26.2; one warp per block that reads the rows past 16 loads twice: 27.1); a few accepted
 // rows each of 8 sequences: 10 us, the launch.
 #include <algorithm>

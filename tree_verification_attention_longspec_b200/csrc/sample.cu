@@ -36,10 +36,10 @@
 // The row is read once from HBM, but HBM does not bound it: a cluster's life is a chain of
 // phases (load, largest, histogram, its sums, borders, weights, decision, find), each behind
 // a cluster barrier, with one shared-memory atomic an entry in the histogram and up to 10
-// fp64 instructions an entry in the weights. Measured (B200): 256 rows of 128,256 bf16 97
+// fp64 instructions an entry in the weights. Measured (B200): 256 rows of 128,256 bf16 96
 // us (0.7 TB/s; the list's way took 238; 53 of them are the loads and barriers alone, as greedy
 // rows show), 123 where the largest logits are 32 or more and `key_map` counts a second time,
-// 64 rows of 152,064 bf16 with the tree walk 32 us, 534 rows of 128,256 with it 168 us, 8 rows
+// 64 rows of 152,064 bf16 with the tree walk 32 us, 534 rows of 128,256 with it 166 us, 8 rows
 // of 32,000 fp32 21 us.
 #include <cooperative_groups.h>
 
